@@ -35,6 +35,11 @@ EXPORTED = (
     "lat_moe_dense_q4_0",
     "lat_moe_dense_q4_0_debug",
     "lat_moe_router_topk",
+    "lat_moe_quantize_fp8",
+    "lat_moe_rmsnorm",
+    "lat_moe_dense_fp8",
+    "lat_moe_ffn_fp8_workspace_size",
+    "lat_moe_ffn_fp8",
     "lat_moe_strerror",
     "lat_moe_version",
 )
@@ -104,6 +109,17 @@ def lib() -> ctypes.CDLL:
         c.lat_moe_dense_q4_0_debug.restype = ctypes.c_int
         c.lat_moe_router_topk.argtypes = [P, i64, i32, i32, P, P, P]
         c.lat_moe_router_topk.restype = ctypes.c_int
+        f32, size = ctypes.c_float, ctypes.c_size_t
+        c.lat_moe_quantize_fp8.argtypes = [P, i32, i64, i32, P, P, P]
+        c.lat_moe_quantize_fp8.restype = ctypes.c_int
+        c.lat_moe_rmsnorm.argtypes = [P, i32, P, i32, P, f32, i64, i32, P, P, i32, P, P, P, P]
+        c.lat_moe_rmsnorm.restype = ctypes.c_int
+        c.lat_moe_dense_fp8.argtypes = [P, P, P, P, i64, i32, i32, P, P, P, P]
+        c.lat_moe_dense_fp8.restype = ctypes.c_int
+        c.lat_moe_ffn_fp8_workspace_size.argtypes = [i64, i32, i32]
+        c.lat_moe_ffn_fp8_workspace_size.restype = size
+        c.lat_moe_ffn_fp8.argtypes = [P, P, P, P, P, P, i64, i32, i32, P, P, P, P, P, size, P]
+        c.lat_moe_ffn_fp8.restype = ctypes.c_int
         c.lat_moe_strerror.argtypes = [ctypes.c_int]
         c.lat_moe_strerror.restype = ctypes.c_char_p
         c.lat_moe_version.restype = ctypes.c_int
@@ -243,6 +259,163 @@ def router_topk(logits, k: int, router_idx, router_w, stream=None) -> None:
     T, E = logits.shape
     _check(lib().lat_moe_router_topk(_ptr(logits), int(T), int(E), int(k), _ptr(router_idx), _ptr(router_w),
                                      _stream(stream)))
+
+
+# ---- e4m3 rows and weights: a scale for each 128 values of a row, or for each 128 x 128 block of a matrix ----
+
+FP8_BLOCK = 128
+
+
+def _types():
+    """torch's element types by what the checks below call them (torch is
+    imported on first use, as everywhere in this module)."""
+    global _TYPES
+    if _TYPES is None:
+        import torch
+        _TYPES = (torch.float8_e4m3fn, torch.float32, torch.bfloat16, torch.uint8,
+                  {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}, torch.cuda.current_device)
+    return _TYPES
+
+
+_TYPES = None
+
+
+def _tensor(name: str, t, dtype, shape, device) -> int:
+    """Data pointer of a contiguous tensor of this type and shape on the
+    current GPU; raises ValueError for anything else."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got "
+                         f"{'' if t.is_contiguous() else 'non-contiguous '}{t.dtype} {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}: expected the current GPU (cuda:{device})")
+    return t.data_ptr()
+
+
+def _device(name: str, t, current_device) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}: expected the current GPU")
+    return current_device()
+
+
+def _rows(name: str, t, kinds) -> int:
+    """The type code of a two-dimensional tensor of rows."""
+    if t.dim() != 2 or t.dtype not in kinds or t.shape[1] >> 31:
+        raise ValueError(f"{name}: expected a 2-dimensional float32, bfloat16 or float16 tensor, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    return kinds[t.dtype]
+
+
+def quantize_fp8(x, codes, scales, stream=None) -> None:
+    """Rows x [rows, cols] (float32, bfloat16 or float16) -> e4m3 codes
+    (float8_e4m3fn [rows, cols]) and scales (float32 [rows, ceil(cols/128)])."""
+    e4m3, f32, _, _, kinds, cur = _types()
+    kind = _rows("x", x, kinds)
+    rows, cols = x.shape
+    dev = _device("x", x, cur)
+    _check(lib().lat_moe_quantize_fp8(_tensor("x", x, x.dtype, (rows, cols), dev), kind, rows, cols,
+                                      _tensor("codes", codes, e4m3, (rows, cols), dev),
+                                      _tensor("scales", scales, f32, (rows, -(-cols // 128)), dev), _stream(stream)))
+
+
+def rmsnorm(x, weight, eps: float, *, residual=None, residual_out=None, y=None, y_q8_1=None, y_fp8=None,
+            y_scales=None, stream=None) -> None:
+    """Root-mean-square norm of x + residual (or of x) with weight (float32
+    [C]), and its roundings: x, residual, residual_out and y are [T, C] in
+    float32, bfloat16 or float16 (residual and residual_out in one type);
+    y_q8_1 is uint8 [T, C/32, 36]; y_fp8 float8_e4m3fn [T, C] with y_scales
+    float32 [T, ceil(C/128)].  Outputs that are None are not made;
+    residual_out may be residual, and y may be x."""
+    e4m3, f32, _, u8, kinds, cur = _types()
+    kind = _rows("x", x, kinds)
+    T, C = shape = x.shape
+    dev = _device("x", x, cur)
+    r_kind = y_kind = 0
+    rp = op = yp = qp = cp = sp = None
+    if residual is not None:
+        r_kind = _rows("residual", residual, kinds)
+        rp = _tensor("residual", residual, residual.dtype, shape, dev)
+    if residual_out is not None:
+        r_kind = _rows("residual_out", residual_out, kinds)
+        op = _tensor("residual_out", residual_out, residual_out.dtype if residual is None else residual.dtype, shape,
+                     dev)
+    if y is not None:
+        y_kind = _rows("y", y, kinds)
+        yp = _tensor("y", y, y.dtype, shape, dev)
+    if y_q8_1 is not None:
+        qp = _tensor("y_q8_1", y_q8_1, u8, (T, C // 32, 36), dev)
+    if y_fp8 is not None:
+        cp = _tensor("y_fp8", y_fp8, e4m3, shape, dev)
+    if y_scales is not None:
+        sp = _tensor("y_scales", y_scales, f32, (T, -(-C // 128)), dev)
+    _check(lib().lat_moe_rmsnorm(_tensor("x", x, x.dtype, shape, dev), kind, rp, r_kind,
+                                 _tensor("weight", weight, f32, (C,), dev), eps, T, C, op, yp, y_kind, qp, cp, sp,
+                                 _stream(stream)))
+
+
+def _matrix(name: str, codes, scales, lead, N: int, K: int, e4m3, f32, dev):
+    """Pointers of an e4m3 matrix: codes [lead * N, K], scales
+    [(lead,) ceil(N/128), ceil(K/128)]."""
+    if N >> 31 or K >> 31:
+        raise ValueError(f"{name}: {N} x {K} is beyond 32-bit sizes")
+    blocks = (-(-N // 128), -(-K // 128))
+    return (_tensor(name, codes, e4m3, ((lead or 1) * N, K), dev),
+            _tensor(name + "'s scales", scales, f32, (lead, *blocks) if lead else blocks, dev))
+
+
+def dense_fp8(x_fp8, x_scales, w_fp8, w_scales, *, y_f32=None, y_bf16=None, y_q8_1=None, stream=None) -> None:
+    """Projection of e4m3 rows x_fp8 (float8_e4m3fn [T, K]) with x_scales
+    (float32 [T, ceil(K/128)]) by e4m3 weights w_fp8 (float8_e4m3fn [N, K])
+    with w_scales (float32 [ceil(N/128), ceil(K/128)]) -> y_f32 (float32
+    [T, N]), y_bf16 (bfloat16 [T, N]) and/or y_q8_1 (uint8 [T, N/32, 36])."""
+    e4m3, f32, bf16, u8, _, cur = _types()
+    if x_fp8.dim() != 2 or w_fp8.dim() != 2:
+        raise ValueError("x_fp8 and w_fp8 have to be 2-dimensional")
+    T, K = x_fp8.shape
+    N = w_fp8.shape[0]
+    dev = _device("x_fp8", x_fp8, cur)
+    w, ws = _matrix("w_fp8", w_fp8, w_scales, 0, N, K, e4m3, f32, dev)
+    _check(lib().lat_moe_dense_fp8(_tensor("x_fp8", x_fp8, e4m3, (T, K), dev),
+                                   _tensor("x_scales", x_scales, f32, (T, -(-K // 128)), dev), w, ws, T, N, K,
+                                   None if y_f32 is None else _tensor("y_f32", y_f32, f32, (T, N), dev),
+                                   None if y_bf16 is None else _tensor("y_bf16", y_bf16, bf16, (T, N), dev),
+                                   None if y_q8_1 is None else _tensor("y_q8_1", y_q8_1, u8, (T, N // 32, 36), dev),
+                                   _stream(stream)))
+
+
+def ffn_fp8_workspace_size(T: int, C: int, F: int) -> int:
+    """Bytes of workspace ffn_fp8 needs (0 if the shapes are unsupported)."""
+    if max(C, F) >> 31:
+        return 0
+    return int(lib().lat_moe_ffn_fp8_workspace_size(int(T), int(C), int(F)))
+
+
+def ffn_fp8(x_fp8, x_scales, gateup_fp8, gateup_scales, down_fp8, down_scales, workspace, *, y_f32=None, y_bf16=None,
+            h_fp8=None, h_scales=None, stream=None) -> None:
+    """Gated feed-forward block on e4m3 rows x_fp8 [T, C] (x_scales [T,
+    ceil(C/128)]): silu(x gate^T) * (x up^T), rounded to e4m3 rows, times
+    down^T.  gateup_fp8 is [2F, C], the gate rows first, with gateup_scales
+    [2, ceil(F/128), ceil(C/128)]; down_fp8 [C, F] with down_scales
+    [ceil(C/128), ceil(F/128)]; y_f32 and/or y_bf16 are [T, C]; h_fp8 [T, F]
+    and h_scales [T, ceil(F/128)] take H if they are given; workspace is a
+    uint8 tensor of at least ffn_fp8_workspace_size(T, C, F) bytes."""
+    e4m3, f32, bf16, u8, _, cur = _types()
+    if x_fp8.dim() != 2 or down_fp8.dim() != 2:
+        raise ValueError("x_fp8 and down_fp8 have to be 2-dimensional")
+    T, C = x_fp8.shape
+    F = down_fp8.shape[1]
+    dev = _device("x_fp8", x_fp8, cur)
+    gu, gus = _matrix("gateup_fp8", gateup_fp8, gateup_scales, 2, F, C, e4m3, f32, dev)
+    dn, dns = _matrix("down_fp8", down_fp8, down_scales, 0, C, F, e4m3, f32, dev)
+    nbytes = workspace.numel()
+    ws = _tensor("workspace", workspace, u8, (nbytes,), dev)
+    _check(lib().lat_moe_ffn_fp8(_tensor("x_fp8", x_fp8, e4m3, (T, C), dev),
+                                 _tensor("x_scales", x_scales, f32, (T, -(-C // 128)), dev), gu, gus, dn, dns, T, C, F,
+                                 None if y_f32 is None else _tensor("y_f32", y_f32, f32, (T, C), dev),
+                                 None if y_bf16 is None else _tensor("y_bf16", y_bf16, bf16, (T, C), dev),
+                                 None if h_fp8 is None else _tensor("h_fp8", h_fp8, e4m3, (T, F), dev),
+                                 None if h_scales is None else _tensor("h_scales", h_scales, f32, (T, -(-F // 128)),
+                                                                       dev),
+                                 ws, nbytes, _stream(stream)))
 
 
 def version() -> int:

@@ -204,6 +204,40 @@ int dense_impl(int wfmt, const void* x_q8_1, const void* w, int64_t T, int32_t N
   return LAT_MOE_OK;
 }
 
+bool type_ok(int32_t t) { return t == LAT_MOE_F32 || t == LAT_MOE_BF16 || t == LAT_MOE_F16; }
+// Columns of e4m3 rows and of the norm: whole 16-byte pieces of codes.
+bool fp8_cols_ok(int32_t cols) { return cols >= 16 && cols <= 65536 && cols % 16 == 0; }
+int64_t fp8_blocks(int64_t n) { return (n + LAT_MOE_FP8_BLOCK - 1) / LAT_MOE_FP8_BLOCK; }
+
+// Shapes of an e4m3 product [T][K] x [N][K]: whole 16-byte pieces of a row, and
+// at most 2^31 output tiles (of 64 x 64, the smallest kind).
+bool fp8_dense_ok(int64_t T, int32_t N, int32_t K) {
+  if (T < 0 || T >= (int64_t)1 << 31 || N < 1 || N > LAT_MOE_FP8_MAX_N || !fp8_cols_ok(K)) return false;
+  return ((T + 63) / 64) * (((int64_t)N + 63) / 64) < (int64_t)1 << 31;
+}
+hipError_t dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int64_t T, int N, int K,
+                     float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus, hipStream_t st) {
+  if (T <= kFp8SmallT) return launch_dense_fp8_small(x, xs, w, ws, (int)T, N, K, y_f32, y_bf16, y_q8, st);
+  return launch_dense_fp8(x, xs, w, ws, T, N, K, y_f32, y_bf16, y_q8, num_cus, st);
+}
+
+bool ffn_fp8_ok(int64_t T, int32_t C, int32_t F) {
+  return fp8_dense_ok(T, F, C) && fp8_dense_ok(T, C, F) && ((T + 63) / 64) * ((F + 31) / 32) < (int64_t)1 << 31;
+}
+// Workspace of the gated block: H's codes and scales, and for few tokens the
+// fp32 H that they are rounded from.
+struct FfnLayout {
+  size_t codes, scales, h32, total;
+};
+FfnLayout ffn_layout(int64_t T, int32_t F) {
+  FfnLayout L{};
+  size_t o = 0;
+  L.codes = o;  o = align_up(o + (size_t)T * F);
+  L.scales = o; o = align_up(o + sizeof(float) * (size_t)(T * fp8_blocks(F)));
+  L.h32 = o;    o = align_up(o + (T <= kFp8SmallT ? sizeof(float) * (size_t)T * F : 0));
+  L.total = o > kAlign ? o : kAlign;
+  return L;
+}
 
 }  // namespace
 
@@ -297,11 +331,115 @@ int lat_moe_router_topk(const float* logits, int64_t T, int32_t E, int32_t k, in
   return LAT_MOE_OK;
 }
 
+int lat_moe_quantize_fp8(const void* x, int32_t x_type, int64_t rows, int32_t cols, void* codes, float* scales,
+                         void* stream) {
+  if (!type_ok(x_type) || rows < 0 || !fp8_cols_ok(cols)) return LAT_MOE_EINVAL;
+  if (rows >= (int64_t)1 << 31 || rows * fp8_blocks(cols) >= (int64_t)1 << 31) return LAT_MOE_EINVAL;
+  if (rows == 0) return LAT_MOE_OK;
+  const void* ptrs[] = {x, codes, scales};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return LAT_MOE_EINVAL;
+  int rc = check_device(nullptr);
+  if (rc != LAT_MOE_OK) return rc;
+  if (launch_quantize_fp8(x, x_type, rows, cols, static_cast<uint8_t*>(codes), scales,
+                          static_cast<hipStream_t>(stream)) != hipSuccess)
+    return LAT_MOE_ELAUNCH;
+  return LAT_MOE_OK;
+}
+
+int lat_moe_rmsnorm(const void* x, int32_t x_type, const void* residual, int32_t residual_type, const float* weight,
+                    float eps, int64_t T, int32_t C, void* residual_out, void* y, int32_t y_type, void* y_q8_1,
+                    void* y_fp8, float* y_scales, void* stream) {
+  if (T < 0 || T >= (int64_t)1 << 31 || !fp8_cols_ok(C) || C > LAT_MOE_NORM_MAX_C || !type_ok(x_type))
+    return LAT_MOE_EINVAL;
+  if (!(eps > 0.f) || eps > 3.402823466e38f) return LAT_MOE_EINVAL;  // NaN and infinity too
+  if ((residual || residual_out) && !type_ok(residual_type)) return LAT_MOE_EINVAL;
+  if (y && !type_ok(y_type)) return LAT_MOE_EINVAL;
+  if (y_q8_1 && C % 32) return LAT_MOE_EINVAL;
+  if (T == 0) return LAT_MOE_OK;
+  if ((y_fp8 == nullptr) != (y_scales == nullptr)) return LAT_MOE_EINVAL;
+  if (!residual_out && !y && !y_q8_1 && !y_fp8) return LAT_MOE_EINVAL;
+  if (!x || !weight) return LAT_MOE_EINVAL;
+  const void* ptrs[] = {x, residual, weight, residual_out, y, y_q8_1, y_fp8, y_scales};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return LAT_MOE_EINVAL;  // null counts as aligned
+  // in place only where an element's place stays its own
+  if (y && y == x && y_type != x_type) return LAT_MOE_EINVAL;
+  int num_cus = 1;
+  int rc = check_device(&num_cus);
+  if (rc != LAT_MOE_OK) return rc;
+  const NormArgs a{x, residual, weight, residual_out, y, static_cast<uint8_t*>(y_q8_1), static_cast<uint8_t*>(y_fp8),
+                   y_scales, T, C, x_type, residual_type, y_type, eps};
+  if (launch_rmsnorm(a, num_cus, static_cast<hipStream_t>(stream)) != hipSuccess) return LAT_MOE_ELAUNCH;
+  return LAT_MOE_OK;
+}
+
+int lat_moe_dense_fp8(const void* x_fp8, const float* x_scales, const void* w_fp8, const float* w_scales, int64_t T,
+                      int32_t N, int32_t K, float* y_f32, void* y_bf16, void* y_q8_1, void* stream) {
+  if (!fp8_dense_ok(T, N, K)) return LAT_MOE_EINVAL;
+  if (y_q8_1 && N % 32) return LAT_MOE_EINVAL;
+  if (T == 0) return LAT_MOE_OK;
+  if (!y_f32 && !y_bf16 && !y_q8_1) return LAT_MOE_EINVAL;
+  const void* need[] = {x_fp8, x_scales, w_fp8, w_scales};
+  for (const void* p : need)
+    if (!p || !aligned16(p)) return LAT_MOE_EINVAL;
+  if (!aligned16(y_f32) || !aligned16(y_bf16) || !aligned16(y_q8_1)) return LAT_MOE_EINVAL;
+  int num_cus = 1;
+  int rc = check_device(&num_cus);
+  if (rc != LAT_MOE_OK) return rc;
+  if (dense_fp8(static_cast<const uint8_t*>(x_fp8), x_scales, static_cast<const uint8_t*>(w_fp8), w_scales, T, N, K,
+                y_f32, static_cast<uint16_t*>(y_bf16), static_cast<uint8_t*>(y_q8_1), num_cus,
+                static_cast<hipStream_t>(stream)) != hipSuccess)
+    return LAT_MOE_ELAUNCH;
+  return LAT_MOE_OK;
+}
+
+size_t lat_moe_ffn_fp8_workspace_size(int64_t T, int32_t C, int32_t F) {
+  return ffn_fp8_ok(T, C, F) ? ffn_layout(T, F).total : 0;
+}
+
+int lat_moe_ffn_fp8(const void* x_fp8, const float* x_scales, const void* gateup_fp8, const float* gateup_scales,
+                    const void* down_fp8, const float* down_scales, int64_t T, int32_t C, int32_t F, float* y_f32,
+                    void* y_bf16, void* h_fp8, float* h_scales, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  if (!ffn_fp8_ok(T, C, F)) return LAT_MOE_EINVAL;
+  if (T == 0) return LAT_MOE_OK;
+  if (!y_f32 && !y_bf16) return LAT_MOE_EINVAL;
+  if ((h_fp8 == nullptr) != (h_scales == nullptr)) return LAT_MOE_EINVAL;
+  const void* need[] = {x_fp8, x_scales, gateup_fp8, gateup_scales, down_fp8, down_scales, workspace};
+  for (const void* p : need)
+    if (!p || !aligned16(p)) return LAT_MOE_EINVAL;
+  if (!aligned16(y_f32) || !aligned16(y_bf16) || !aligned16(h_fp8) || !aligned16(h_scales)) return LAT_MOE_EINVAL;
+  const FfnLayout L = ffn_layout(T, F);
+  if (workspace_bytes < L.total) return LAT_MOE_EWORKSPACE;
+  int num_cus = 1;
+  int rc = check_device(&num_cus);
+  if (rc != LAT_MOE_OK) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  const uint8_t* x = static_cast<const uint8_t*>(x_fp8);
+  const uint8_t* gu = static_cast<const uint8_t*>(gateup_fp8);
+  uint8_t* h = h_fp8 ? static_cast<uint8_t*>(h_fp8) : reinterpret_cast<uint8_t*>(ws + L.codes);
+  float* hs = h_fp8 ? h_scales : reinterpret_cast<float*>(ws + L.scales);
+  if (T <= kFp8SmallT) {
+    float* h32 = reinterpret_cast<float*>(ws + L.h32);
+    if (launch_gateup_fp8_small(x, x_scales, gu, gateup_scales, (int)T, F, C, h32, st) != hipSuccess ||
+        launch_quantize_fp8(h32, LAT_MOE_F32, T, F, h, hs, st) != hipSuccess)
+      return LAT_MOE_ELAUNCH;
+  } else if (launch_gateup_fp8(x, x_scales, gu, gateup_scales, T, F, C, h, hs, num_cus, st) != hipSuccess) {
+    return LAT_MOE_ELAUNCH;
+  }
+  if (dense_fp8(h, hs, static_cast<const uint8_t*>(down_fp8), down_scales, T, C, F, y_f32,
+                static_cast<uint16_t*>(y_bf16), nullptr, num_cus, st) != hipSuccess)
+    return LAT_MOE_ELAUNCH;
+  return LAT_MOE_OK;
+}
+
 const char* lat_moe_strerror(int code) {
   switch (code) {
     case LAT_MOE_OK: return "ok";
     case LAT_MOE_EINVAL: return "invalid argument (null or misaligned pointer, or unsupported shape)";
-    case LAT_MOE_EWORKSPACE: return "workspace smaller than lat_moe_workspace_size()";
+    case LAT_MOE_EWORKSPACE: return "workspace smaller than the entry point's workspace size";
     case LAT_MOE_EDEVICE: return "current device is not a gfx950 with 64-wide wavefronts";
     case LAT_MOE_ELAUNCH: return "kernel launch failed";
     case LAT_MOE_ESCRATCH: return "shapes need more workspace than the no-allocation entry point's fixed scratch";
@@ -309,6 +447,6 @@ const char* lat_moe_strerror(int code) {
   }
 }
 
-int lat_moe_version(void) { return 100; }
+int lat_moe_version(void) { return 200; }
 
 }  // extern "C"

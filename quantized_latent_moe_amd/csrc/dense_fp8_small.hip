@@ -1,0 +1,185 @@
+// Products of e4m3 rows with e4m3 weights for at most kFp8SmallT tokens
+// (decode): the formulas of the tile kernel, arranged to stream the weights.
+//
+// Each weight is used for a few tokens only, so the time is that of reading
+// the weights once, and the products are exact: codes are widened to bf16 for
+// the bf16 MFMA, whatever the output type.  A workgroup takes 16 FR weight rows whole: its 8 waves
+// deal the blocks of K = 128 among themselves, load fragments straight from
+// memory into registers (no LDS on the way in; a lane's two 16-byte pieces lie
+// 64 bytes apart, so each load covers 64 contiguous bytes of a row), several
+// blocks ahead, and add their partial sums in LDS at the end, in wave order:
+// the result does not depend on timing.
+#include "block_fp8.h"
+
+namespace latmoe {
+namespace {
+
+constexpr int kWaves = 8;
+
+struct SmallArgs {
+  const uint8_t* x;
+  const float* xs;
+  const uint8_t* w;
+  const float* ws;
+  float* y_f32;
+  uint16_t* y_bf16;
+  uint8_t* y_q8;
+  int T, N, K, nb;
+};
+
+// Two 16-byte pieces of codes to four bf16 operands.
+__device__ __forceinline__ void widen16(const uint4* p, v8bf* o) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    o[2 * h] = widen((int)p[h].x, (int)p[h].y);
+    o[2 * h + 1] = widen((int)p[h].z, (int)p[h].w);
+  }
+}
+
+// Token columns past T and weight rows past N hold zeros or a clamped row;
+// they meet only results that are not stored.
+template <int FR, int TF, bool GATED>
+__global__ __launch_bounds__(64 * kWaves) void k_dense_fp8_small(const SmallArgs a) {
+  constexpr int U = TF == 1 ? 4 : 2;  // blocks in flight per wave
+  constexpr int NF = GATED ? 16 : 16 * FR;  // output columns
+  static_assert(!GATED || FR == 2, "a gate fragment and its up fragment");
+  __shared__ __align__(16) float red[kWaves][FR * TF][64][4];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int n0 = (int)blockIdx.x * NF;
+  const int K = a.K, nb = a.nb;
+  const int nbn = (a.N + kFp8Block - 1) / kFp8Block;
+
+  rsrc_t rw[FR];
+  int wrow[FR], wblk[FR];
+#pragma unroll
+  for (int i = 0; i < FR; ++i) {
+    const int first = GATED ? n0 : n0 + 16 * i;  // of the fragment's 16 rows
+    const int base = min(first, a.N - 1);
+    rw[i] = make_rsrc(a.w + ((GATED && i ? (int64_t)a.N : 0) + base) * K, (uint32_t)min(16, a.N - base) * K);
+    wrow[i] = min(r, a.N - 1 - base) * K;
+    wblk[i] = ((GATED && i ? nbn : 0) + base / kFp8Block) * nb;
+  }
+  const rsrc_t rx = make_rsrc(a.x, (uint32_t)a.T * K);
+  const rsrc_t rs = make_rsrc(a.xs, (uint32_t)a.T * nb * 4);
+  const rsrc_t rws = make_rsrc(a.ws, (uint32_t)((GATED ? 2 : 1) * nbn * nb) * 4u);
+
+  v4f acc[FR][TF] = {};
+  for (int k0 = wave; k0 < nb; k0 += U * kWaves) {
+    uint4 wa[U][FR][2], xa[U][TF][2];
+    float sx[U][TF], sw[U][FR];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = k0 + u * kWaves;
+      const int c0 = kb * kFp8Block + 16 * g, c1 = c0 + 64;
+      const bool in0 = c0 < K, in1 = c1 < K;  // false past the row's end, and so for every block past the last
+#pragma unroll
+      for (int i = 0; i < FR; ++i) {
+        wa[u][i][0] = buf_u128(rw[i], in0 ? wrow[i] + c0 : kOutOfRange, 0);
+        wa[u][i][1] = buf_u128(rw[i], in1 ? wrow[i] + c1 : kOutOfRange, 0);
+        sw[u][i] = __builtin_bit_cast(float, buf_u32(rws, kb < nb ? (wblk[i] + kb) * 4 : kOutOfRange, 0));
+      }
+#pragma unroll
+      for (int j = 0; j < TF; ++j) {
+        const int t = 16 * j + r;
+        xa[u][j][0] = buf_u128(rx, in0 && t < a.T ? t * K + c0 : kOutOfRange, 0);
+        xa[u][j][1] = buf_u128(rx, in1 && t < a.T ? t * K + c1 : kOutOfRange, 0);
+        sx[u][j] = __builtin_bit_cast(float, buf_u32(rs, kb < nb && t < a.T ? (t * nb + kb) * 4 : kOutOfRange, 0));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < FR; ++i) {
+        v8bf fa[4];
+        widen16(wa[u][i], fa);
+#pragma unroll
+        for (int j = 0; j < TF; ++j) {
+          v8bf fb[4];
+          widen16(xa[u][j], fb);
+          v4f d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[q], fb[q], d, 0, 0, 0);
+          const float s = sx[u][j] * sw[u][i];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(s, d[e], acc[i][j][e]);
+        }
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < FR; ++i)
+#pragma unroll
+    for (int j = 0; j < TF; ++j) *reinterpret_cast<v4f*>(red[wave][i * TF + j][lane]) = acc[i][j];
+  __syncthreads();
+
+  // column c of token t: fragment (c / 16, t / 16), lane 16 (c % 16 / 4) + t % 16, element c % 4
+  auto total = [&](int c, int t) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+      s += red[w][(c >> 4) * TF + (t >> 4)][((c & 15) >> 2) * 16 + (t & 15)][c & 3];
+    return s;
+  };
+  for (int o = tid; o < NF * 16 * TF; o += 64 * kWaves) {
+    const int t = o / NF, c = o % NF, n = n0 + c;
+    const bool live = t < a.T && n < a.N;  // a whole 32-column block of a token, or none of it, where N % 32 == 0
+    float v = total(c, t);
+    if constexpr (GATED) {
+      const float u = total(16 + c, t);
+      v = v / (1.0f + __expf(-v)) * u;
+    }
+    if (live && a.y_f32) a.y_f32[(int64_t)t * a.N + n] = v;
+    if (live && a.y_bf16) a.y_bf16[(int64_t)t * a.N + n] = (uint16_t)pack_bf16(v, v);
+    if constexpr (!GATED && FR == 2) {
+#pragma clang fp contract(off)
+      if (a.y_q8) {
+        // 32 lanes hold one q8_1 block
+        float amax = fabsf(v);
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) amax = fmaxf(amax, __shfl_xor(amax, s));
+        const float d = amax / 127.0f;
+        const float id = d != 0.0f ? 1.0f / d : 0.0f;
+        const int q = round_half_away(v * id);
+        int sum = q;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) sum += __shfl_xor(sum, s);
+        if (live) {
+          uint8_t* blk = a.y_q8 + ((int64_t)t * (a.N / 32) + n / 32) * kQ81Bytes;
+          blk[4 + c] = (uint8_t)q;
+          if (c == 0)
+            *reinterpret_cast<uint32_t*>(blk) =
+                float_to_half_bits(d) | (float_to_half_bits(fp32_barrier(d * (float)sum)) << 16);
+        }
+      }
+    }
+  }
+}
+
+template <int FR, bool GATED>
+void run(const SmallArgs& a, hipStream_t st) {
+  const int nf = GATED ? 16 : 16 * FR;
+  const dim3 grid((unsigned)((a.N + nf - 1) / nf)), block(64 * kWaves);
+  if (a.T <= 16) hipLaunchKernelGGL((k_dense_fp8_small<FR, 1, GATED>), grid, block, 0, st, a);
+  else if (a.T <= 32) hipLaunchKernelGGL((k_dense_fp8_small<FR, 2, GATED>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_dense_fp8_small<FR, 4, GATED>), grid, block, 0, st, a);
+}
+
+}  // namespace
+
+hipError_t launch_dense_fp8_small(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int T, int N,
+                                  int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, hipStream_t st) {
+  const SmallArgs a{x, xs, w, ws, y_f32, y_bf16, y_q8, T, N, K, (K + kFp8Block - 1) / kFp8Block};
+  if (y_q8) run<2, false>(a, st);  // a q8_1 block is 32 columns
+  else run<1, false>(a, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_gateup_fp8_small(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int T,
+                                   int F, int C, float* h, hipStream_t st) {
+  run<2, true>(SmallArgs{x, xs, gu, gus, h, nullptr, nullptr, T, F, C, (C + kFp8Block - 1) / kFp8Block}, st);
+  return hipGetLastError();
+}
+
+}  // namespace latmoe

@@ -233,4 +233,36 @@ bool dense_ws_shape(int N, int K);
 hipError_t launch_dense_ws(const uint8_t* x, const uint8_t* w, int wfmt, int64_t T, int N, int K, float* y_f32,
                            uint8_t* y_q8, const ProbeRows* probe, int num_cus, hipStream_t st);
 
+// Rows to e4m3 with a scale for each 128 values.
+hipError_t launch_quantize_fp8(const void* x, int x_type, int64_t rows, int cols, uint8_t* codes, float* scales,
+                               hipStream_t st);
+// Residual addition, root-mean-square norm and its 8-bit roundings (any output may be null).
+struct NormArgs {
+  const void* x;
+  const void* residual;
+  const float* weight;
+  void* residual_out;
+  void* y;
+  uint8_t* y_q8;
+  uint8_t* y_fp8;
+  float* y_scales;
+  int64_t T;
+  int C, x_type, residual_type, y_type;
+  float eps;
+};
+hipError_t launch_rmsnorm(const NormArgs& a, int num_cus, hipStream_t st);
+// e4m3 rows [T][K] x e4m3 weights [N][K] -> y in fp32, bf16 and/or q8_1 (any may be null, not all).
+hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int64_t T, int N,
+                            int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus, hipStream_t st);
+// The same for at most kFp8SmallT tokens, by a kernel that streams the weights.
+constexpr int kFp8SmallT = 64;
+hipError_t launch_dense_fp8_small(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int T, int N,
+                                  int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, hipStream_t st);
+// silu(G) * U of at most kFp8SmallT tokens, unrounded: h [T][F] fp32.
+hipError_t launch_gateup_fp8_small(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int T,
+                                   int F, int C, float* h, hipStream_t st);
+// Gate and up projections (gu [2F][C]: gate rows, then up rows), silu(G) * U, rounded to e4m3 rows h [T][F].
+hipError_t launch_gateup_fp8(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int64_t T, int F,
+                             int C, uint8_t* h, float* hs, int num_cus, hipStream_t st);
+
 }  // namespace latmoe
