@@ -266,29 +266,32 @@ def router_topk(logits, k: int, router_idx, router_w, stream=None) -> None:
 FP8_BLOCK = 128
 
 
-def _types():
-    """torch's element types by what the checks below call them (torch is
-    imported on first use, as everywhere in this module)."""
-    global _TYPES
-    if _TYPES is None:
+_TORCH = None
+
+
+def _torch():
+    """What the calls below use of torch (imported on first use, as everywhere
+    in this module): element types, the type codes of rows, and the current
+    device's index and its current stream's handle."""
+    global _TORCH
+    if _TORCH is None:
         import torch
-        _TYPES = (torch.float8_e4m3fn, torch.float32, torch.bfloat16, torch.uint8,
-                  {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}, torch.cuda.current_device)
-    return _TYPES
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # about 0.1 us, a Stream object about 3
+        _TORCH = (torch.float8_e4m3fn, torch.float32, torch.bfloat16, torch.uint8,
+                  {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}, torch.cuda.current_device,
+                  raw or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+    return _TORCH
 
 
-_TYPES = None
-
-
-def _tensor(name: str, t, dtype, shape, device) -> int:
+def _tensor(name: str, t, dtype, shape, device: int) -> int:
     """Data pointer of a contiguous tensor of this type and shape on the
     current GPU; raises ValueError for anything else."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got "
-                         f"{'' if t.is_contiguous() else 'non-contiguous '}{t.dtype} {tuple(t.shape)}")
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}: expected the current GPU (cuda:{device})")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got "
+                     f"{'' if t.is_contiguous() else 'non-contiguous '}{t.dtype} {tuple(t.shape)}")
 
 
 def _device(name: str, t, current_device) -> int:
@@ -308,13 +311,16 @@ def _rows(name: str, t, kinds) -> int:
 def quantize_fp8(x, codes, scales, stream=None) -> None:
     """Rows x [rows, cols] (float32, bfloat16 or float16) -> e4m3 codes
     (float8_e4m3fn [rows, cols]) and scales (float32 [rows, ceil(cols/128)])."""
-    e4m3, f32, _, _, kinds, cur = _types()
+    e4m3, f32, _, _, kinds, cur, raw = _torch()
     kind = _rows("x", x, kinds)
-    rows, cols = x.shape
+    rows, cols = shape = x.shape
     dev = _device("x", x, cur)
-    _check(lib().lat_moe_quantize_fp8(_tensor("x", x, x.dtype, (rows, cols), dev), kind, rows, cols,
-                                      _tensor("codes", codes, e4m3, (rows, cols), dev),
-                                      _tensor("scales", scales, f32, (rows, -(-cols // 128)), dev), _stream(stream)))
+    rc = lib().lat_moe_quantize_fp8(_tensor("x", x, x.dtype, shape, dev), kind, rows, cols,
+                                    _tensor("codes", codes, e4m3, shape, dev),
+                                    _tensor("scales", scales, f32, (rows, -(-cols // 128)), dev),
+                                    raw(dev) if stream is None else int(stream))
+    if rc:
+        _check(rc)
 
 
 def rmsnorm(x, weight, eps: float, *, residual=None, residual_out=None, y=None, y_q8_1=None, y_fp8=None,
@@ -325,7 +331,7 @@ def rmsnorm(x, weight, eps: float, *, residual=None, residual_out=None, y=None, 
     y_q8_1 is uint8 [T, C/32, 36]; y_fp8 float8_e4m3fn [T, C] with y_scales
     float32 [T, ceil(C/128)].  Outputs that are None are not made;
     residual_out may be residual, and y may be x."""
-    e4m3, f32, _, u8, kinds, cur = _types()
+    e4m3, f32, _, u8, kinds, cur, raw = _torch()
     kind = _rows("x", x, kinds)
     T, C = shape = x.shape
     dev = _device("x", x, cur)
@@ -347,9 +353,11 @@ def rmsnorm(x, weight, eps: float, *, residual=None, residual_out=None, y=None, 
         cp = _tensor("y_fp8", y_fp8, e4m3, shape, dev)
     if y_scales is not None:
         sp = _tensor("y_scales", y_scales, f32, (T, -(-C // 128)), dev)
-    _check(lib().lat_moe_rmsnorm(_tensor("x", x, x.dtype, shape, dev), kind, rp, r_kind,
-                                 _tensor("weight", weight, f32, (C,), dev), eps, T, C, op, yp, y_kind, qp, cp, sp,
-                                 _stream(stream)))
+    rc = lib().lat_moe_rmsnorm(_tensor("x", x, x.dtype, shape, dev), kind, rp, r_kind,
+                               _tensor("weight", weight, f32, (C,), dev), eps, T, C, op, yp, y_kind, qp, cp, sp,
+                               raw(dev) if stream is None else int(stream))
+    if rc:
+        _check(rc)
 
 
 def _matrix(name: str, codes, scales, lead, N: int, K: int, e4m3, f32, dev):
@@ -367,19 +375,21 @@ def dense_fp8(x_fp8, x_scales, w_fp8, w_scales, *, y_f32=None, y_bf16=None, y_q8
     (float32 [T, ceil(K/128)]) by e4m3 weights w_fp8 (float8_e4m3fn [N, K])
     with w_scales (float32 [ceil(N/128), ceil(K/128)]) -> y_f32 (float32
     [T, N]), y_bf16 (bfloat16 [T, N]) and/or y_q8_1 (uint8 [T, N/32, 36])."""
-    e4m3, f32, bf16, u8, _, cur = _types()
+    e4m3, f32, bf16, u8, _, cur, raw = _torch()
     if x_fp8.dim() != 2 or w_fp8.dim() != 2:
         raise ValueError("x_fp8 and w_fp8 have to be 2-dimensional")
-    T, K = x_fp8.shape
+    T, K = shape = x_fp8.shape
     N = w_fp8.shape[0]
     dev = _device("x_fp8", x_fp8, cur)
     w, ws = _matrix("w_fp8", w_fp8, w_scales, 0, N, K, e4m3, f32, dev)
-    _check(lib().lat_moe_dense_fp8(_tensor("x_fp8", x_fp8, e4m3, (T, K), dev),
-                                   _tensor("x_scales", x_scales, f32, (T, -(-K // 128)), dev), w, ws, T, N, K,
-                                   None if y_f32 is None else _tensor("y_f32", y_f32, f32, (T, N), dev),
-                                   None if y_bf16 is None else _tensor("y_bf16", y_bf16, bf16, (T, N), dev),
-                                   None if y_q8_1 is None else _tensor("y_q8_1", y_q8_1, u8, (T, N // 32, 36), dev),
-                                   _stream(stream)))
+    rc = lib().lat_moe_dense_fp8(_tensor("x_fp8", x_fp8, e4m3, shape, dev),
+                                 _tensor("x_scales", x_scales, f32, (T, -(-K // 128)), dev), w, ws, T, N, K,
+                                 None if y_f32 is None else _tensor("y_f32", y_f32, f32, (T, N), dev),
+                                 None if y_bf16 is None else _tensor("y_bf16", y_bf16, bf16, (T, N), dev),
+                                 None if y_q8_1 is None else _tensor("y_q8_1", y_q8_1, u8, (T, N // 32, 36), dev),
+                                 raw(dev) if stream is None else int(stream))
+    if rc:
+        _check(rc)
 
 
 def ffn_fp8_workspace_size(T: int, C: int, F: int) -> int:
@@ -398,24 +408,26 @@ def ffn_fp8(x_fp8, x_scales, gateup_fp8, gateup_scales, down_fp8, down_scales, w
     [ceil(C/128), ceil(F/128)]; y_f32 and/or y_bf16 are [T, C]; h_fp8 [T, F]
     and h_scales [T, ceil(F/128)] take H if they are given; workspace is a
     uint8 tensor of at least ffn_fp8_workspace_size(T, C, F) bytes."""
-    e4m3, f32, bf16, u8, _, cur = _types()
+    e4m3, f32, bf16, u8, _, cur, raw = _torch()
     if x_fp8.dim() != 2 or down_fp8.dim() != 2:
         raise ValueError("x_fp8 and down_fp8 have to be 2-dimensional")
-    T, C = x_fp8.shape
+    T, C = shape = x_fp8.shape
     F = down_fp8.shape[1]
     dev = _device("x_fp8", x_fp8, cur)
     gu, gus = _matrix("gateup_fp8", gateup_fp8, gateup_scales, 2, F, C, e4m3, f32, dev)
     dn, dns = _matrix("down_fp8", down_fp8, down_scales, 0, C, F, e4m3, f32, dev)
     nbytes = workspace.numel()
-    ws = _tensor("workspace", workspace, u8, (nbytes,), dev)
-    _check(lib().lat_moe_ffn_fp8(_tensor("x_fp8", x_fp8, e4m3, (T, C), dev),
-                                 _tensor("x_scales", x_scales, f32, (T, -(-C // 128)), dev), gu, gus, dn, dns, T, C, F,
-                                 None if y_f32 is None else _tensor("y_f32", y_f32, f32, (T, C), dev),
-                                 None if y_bf16 is None else _tensor("y_bf16", y_bf16, bf16, (T, C), dev),
-                                 None if h_fp8 is None else _tensor("h_fp8", h_fp8, e4m3, (T, F), dev),
-                                 None if h_scales is None else _tensor("h_scales", h_scales, f32, (T, -(-F // 128)),
-                                                                       dev),
-                                 ws, nbytes, _stream(stream)))
+    rc = lib().lat_moe_ffn_fp8(_tensor("x_fp8", x_fp8, e4m3, shape, dev),
+                               _tensor("x_scales", x_scales, f32, (T, -(-C // 128)), dev), gu, gus, dn, dns, T, C, F,
+                               None if y_f32 is None else _tensor("y_f32", y_f32, f32, shape, dev),
+                               None if y_bf16 is None else _tensor("y_bf16", y_bf16, bf16, shape, dev),
+                               None if h_fp8 is None else _tensor("h_fp8", h_fp8, e4m3, (T, F), dev),
+                               None if h_scales is None else _tensor("h_scales", h_scales, f32, (T, -(-F // 128)),
+                                                                     dev),
+                               _tensor("workspace", workspace, u8, (nbytes,), dev), nbytes,
+                               raw(dev) if stream is None else int(stream))
+    if rc:
+        _check(rc)
 
 
 def version() -> int:

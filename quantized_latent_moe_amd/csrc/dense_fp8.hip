@@ -38,15 +38,38 @@ typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int kXcds = 8;
 constexpr int kStep = kFp8Block;  // K per step: one MFMA, one scale
-constexpr int kScaleSteps = 4;    // steps whose scales are staged together
+constexpr int kScaleShift = 2, kScaleSteps = 1 << kScaleShift;  // steps whose scales are staged together
 
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 
-// Wait for this wave's outstanding loads, then for the workgroup.
-__device__ __forceinline__ void loads_done_barrier() {
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-  __syncthreads();
+// 4 x 4 transpose between four registers and the four 16-lane groups of a
+// wave: register k of group g becomes register g of group k.
+__device__ __forceinline__ void transpose4(uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto v = __builtin_amdgcn_permlane32_swap(r[i], r[i + 2], false, false);
+    r[i] = v[0];
+    r[i + 2] = v[1];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const auto v = __builtin_amdgcn_permlane16_swap(r[i], r[i + 1], false, false);
+    r[i] = v[0];
+    r[i + 1] = v[1];
+  }
 }
+
+// Wait until at most N of this wave's loads and none of its LDS accesses are
+// outstanding, then for the workgroup.  (__syncthreads waits for every load,
+// those of later steps too.)
+template <int N>
+__device__ __forceinline__ void loads_done_barrier() {
+  static_assert(N < 64, "vmcnt has 6 bits");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// The workgroup's barrier for LDS alone: stores to memory go on.
+__device__ __forceinline__ void lds_barrier() { loads_done_barrier<63>(); }
 
 struct DenseArgs {
   const uint8_t* x;   // [T][K] e4m3
@@ -83,19 +106,17 @@ __device__ __forceinline__ void tile_of(const DenseArgs& a, int& nt, int& tt) {
 // projection with bf16 products, or the gated pair of projections.
 enum Mode : int { kFast = 0, kExact = 1, kGated = 2 };
 
-template <int FA, int FB, int WN, int WT, int MODE>
+template <int FA, int FB, int WN, int WT, int MODE, int STAGES>
 struct Tile {
   static constexpr bool GATED = MODE == kGated;
   static constexpr int kThreads = 64 * WN * WT;
   static constexpr int TN = 16 * FA * WN, TT = 16 * FB * WT;
   static constexpr int kWaves = WN * WT;
   static constexpr int kLoadsA = TN / 8 / kWaves, kLoadsB = TT / 8 / kWaves;  // 1 KB each
-  // a tile's weight rows lie in kSets scale blocks (gated: the gate's and the up's)
-  static constexpr int kSets = GATED ? 2 : TN <= kFp8Block ? 1 : TN / kFp8Block;
-  static constexpr int kScalesPerThread = kScaleSteps * TT / kThreads;
-  static_assert(kScalesPerThread >= 1 && kScaleSteps % kScalesPerThread == 0, "whole runs of scales");
   static_assert(kFp8Block % (16 * FA) == 0, "a wave's weight rows lie in one scale block");
   static_assert(TN % (8 * kWaves) == 0 && TT % (8 * kWaves) == 0, "whole loads");
+  static_assert(TT % 64 == 0 && TT / 64 <= kWaves, "a wave loads 64 tokens' scales");
+  static_assert(STAGES == 2 || STAGES == 3, "one or two steps ahead");
   static_assert(!GATED || TN == 256, "a gated tile holds one e4m3 block of H");
 
   // H column (within the tile) of LDS row r of the weight tile, gated tiles:
@@ -107,27 +128,35 @@ struct Tile {
   }
   static __device__ __forceinline__ bool gated_up(int r) { return (r % (16 * FA)) >= 8 * FA; }
 
-  // Direct loads of one K step into LDS.
-  static __device__ __forceinline__ void load_tiles(rsrc_t ra, rsrc_t ru, rsrc_t rb, uint8_t* __restrict__ As,
-                                                    uint8_t* __restrict__ Bs, const int* va, const int* vb, int k0,
+  // What a wave loads: the tile's buffers (weight rows, gated: the up rows,
+  // tokens, scales; rows past the end lie past the buffer's records: their
+  // loads return zeros), and the lane's byte offset in each of its pieces at
+  // K step 0.  Only the step's start, in the scalar offset, changes.
+  struct Source {
+    rsrc_t w, up, x, xs;
+    int vw[kLoadsA], vx[kLoadsB], vs;
+  };
+  // The wave's j-th direct load of a K step into LDS: weight rows, then tokens.
+  static constexpr int kLoads = kLoadsA + kLoadsB;
+  static __device__ __forceinline__ void load_piece(int j, const Source& src, uint8_t* As, uint8_t* Bs, int k0,
                                                     int wave) {
-#pragma unroll
-    for (int j = 0; j < kLoadsA; ++j) {
+    if (j < kLoadsA) {
       const int piece = wave * kLoadsA + j;  // rows 8 piece .. +7
-      const bool up = GATED && gated_up(8 * piece);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(up ? ru : ra, (lds_void*)(As + piece * 1024), 16, va[j], k0, 0, 0);
-    }
-#pragma unroll
-    for (int j = 0; j < kLoadsB; ++j) {
-      const int piece = wave * kLoadsB + j;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(Bs + piece * 1024), 16, vb[j], k0, 0, 0);
+      const rsrc_t r = GATED && gated_up(8 * piece) ? src.up : src.w;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(As + piece * 1024), 16, src.vw[j], k0, 0, 0);
+    } else {
+      const int piece = wave * kLoadsB + j - kLoadsA;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(src.x, (lds_void*)(Bs + piece * 1024), 16, src.vx[j - kLoadsA], k0, 0,
+                                               0);
     }
   }
 
   static __device__ __forceinline__ v8i fragment(const uint8_t* s, int row, int g) {
-    // chunks 2g, 2g + 1 of the row: the same K order in both operands
-    const v4i lo = *reinterpret_cast<const v4i*>(s + row * kStep + (((2 * g) ^ swz(row)) << 4));
-    const v4i hi = *reinterpret_cast<const v4i*>(s + row * kStep + (((2 * g + 1) ^ swz(row)) << 4));
+    // chunks g and g + 4 of the row: the same K order in both operands, and no
+    // two of the lanes that LDS serves together meet in a bank (chunks 2g and
+    // 2g + 1 with this swizzle do, at half the read rate)
+    const v4i lo = *reinterpret_cast<const v4i*>(s + row * kStep + ((g ^ swz(row)) << 4));
+    const v4i hi = *reinterpret_cast<const v4i*>(s + row * kStep + (((g + 4) ^ swz(row)) << 4));
     return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   }
 
@@ -136,8 +165,7 @@ struct Tile {
   struct Codes { v8i v; };
   struct Wide { v8bf v[4]; };
   using Operand = std::conditional_t<MODE == kExact, Wide, Codes>;
-  static __device__ __forceinline__ Operand operand(const uint8_t* s, int row, int g) {
-    const v8i f = fragment(s, row, g);
+  static __device__ __forceinline__ Operand operand(v8i f) {
     if constexpr (MODE == kExact) {
       Wide o;
 #pragma unroll
@@ -158,33 +186,46 @@ struct Tile {
     return p;
   }
 
-  // The step's products.  The MFMA of fragment pair q is issued before the
-  // fold of pair q - kLag, whose result is then complete, and the weight
-  // fragment of the next row of pairs is read meanwhile.
-  static constexpr int kLag = 2;
-  static __device__ __forceinline__ void multiply(const uint8_t* __restrict__ As, const uint8_t* __restrict__ Bs,
-                                                  const float* __restrict__ sx, v4f (*acc)[FB], int wn, int wt,
-                                                  int lane) {
+  // The step's products, and the direct loads of a later one.  The MFMA of
+  // fragment pair q is issued before the fold of pair q - kLag, whose result
+  // is then complete; weight fragments are read two rows of pairs ahead, and
+  // the loads are spread over the pairs (issued together at the step's start
+  // they hold the wave back until the memory pipe has taken them).
+  static constexpr int kLag = 4;
+  template <class Load>
+  static __device__ __forceinline__ void multiply(const uint8_t* As, const uint8_t* Bs, const float* sx, float sw0,
+                                                  float sw1, v4f (*acc)[FB], int wn, int wt, int lane, Load load) {
     const int r = lane & 15, g = lane >> 4;
     const int a_row = wn * 16 * FA + r, b_row = wt * 16 * FB + r;
-    const int set = kSets == 1 || GATED ? 0 : wn * 16 * FA / kFp8Block;
-    Operand b[FB], a[2];
+    v8i a[3], bf[FB];
+    Operand ao, b[FB];
     float s[GATED ? 2 : 1][FB];
-    a[0] = operand(As, a_row, g);
+    a[0] = fragment(As, a_row, g);
 #pragma unroll
-    for (int j = 0; j < FB; ++j) b[j] = operand(Bs, b_row + 16 * j, g);
+    for (int j = 0; j < FB; ++j) bf[j] = fragment(Bs, b_row + 16 * j, g);
+    a[1] = fragment(As, a_row + 16, g);
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
-      s[0][j] = sx[set * TT + b_row + 16 * j];
-      if (GATED) s[GATED][j] = sx[TT + b_row + 16 * j];
+      const float x = sx[(b_row + 16 * j) * kScaleSteps];
+      s[0][j] = x * sw0;
+      if (GATED) s[GATED][j] = x * sw1;
     }
+#pragma unroll
+    for (int j = 0; j < FB; ++j) b[j] = operand(bf[j]);
     v4f p[kLag + 1];
 #pragma unroll
     for (int q = 0; q < FA * FB + kLag; ++q) {
       if (q < FA * FB) {
         const int i = q / FB, j = q % FB;
-        if (j == 0 && i + 1 < FA) a[(i + 1) & 1] = operand(As, a_row + 16 * (i + 1), g);
-        p[q % (kLag + 1)] = product(a[i & 1], b[j]);
+        if (j == 0) {
+          if (i + 2 < FA) a[(i + 2) % 3] = fragment(As, a_row + 16 * (i + 2), g);
+          ao = operand(a[i % 3]);
+        }
+        p[q % (kLag + 1)] = product(ao, b[j]);
+        // load l goes after pair l * pairs / loads
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l)
+          if (l * (FA * FB) / 2 / kLoads == q) load(l);
       }
       if (q >= kLag) {
         const int i = (q - kLag) / FB, j = (q - kLag) % FB;
@@ -192,44 +233,45 @@ struct Tile {
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(f, p[(q - kLag) % (kLag + 1)][e], acc[i][j][e]);
       }
+      __builtin_amdgcn_sched_barrier(0);  // the scheduler keeps this order
     }
     // the folds stay in this step (the compiler would sink them past the next branch)
 #pragma unroll
     for (int i = 0; i < FA; ++i)
 #pragma unroll
       for (int j = 0; j < FB; ++j) asm volatile("" : "+v"(acc[i][j]));
-    if constexpr (MODE != kExact) {
-      // the order above, as the scheduler is to keep it
-#pragma unroll
-      for (int q = 0; q < FA * FB + kLag; ++q) {
-        if (q < FA * FB) {
-          if (q % FB == 0 && q / FB + 1 < FA) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                      // MFMA
-        }
-        if (q >= kLag) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // VALU
-      }
-    }
   }
 
-  // One step: the next step's loads into the other buffers, then this step's products.
-  static __device__ __forceinline__ void step(bool more, rsrc_t ra, rsrc_t ru, rsrc_t rb,
+  // One step: a later step's tiles and a later run's scales (k_s: their byte
+  // offset in a row, or negative) on their way into other buffers, and this
+  // step's products.  Every LDS access of the main loop is in here, behind
+  // pointers that do not overlap (__restrict__), and the loop's first rounds
+  // only load: the compiler then sees that no read touches what a direct load
+  // in flight writes, and adds no wait of its own.
+  static __device__ __forceinline__ void step(bool products, const Source& src, int k_load, int k_s,
                                               const uint8_t* __restrict__ As, const uint8_t* __restrict__ Bs,
-                                              uint8_t* __restrict__ An, uint8_t* __restrict__ Bn,
-                                              const float* __restrict__ sx, const int* va, const int* vb, int k_next,
+                                              const float* __restrict__ sx, uint8_t* __restrict__ An,
+                                              uint8_t* __restrict__ Bn, float* __restrict__ sn, float sw0, float sw1,
                                               v4f (*acc)[FB], int wave, int wn, int wt, int lane) {
-    if (more) load_tiles(ra, ru, rb, An, Bn, va, vb, k_next, wave);
-    multiply(As, Bs, sx, acc, wn, wt, lane);
+    auto load = [&](int j) { load_piece(j, src, An, Bn, k_load, wave); };
+    if (k_s >= 0) __builtin_amdgcn_raw_ptr_buffer_load_lds(src.xs, (lds_void*)sn, 16, src.vs + k_s, 0, 0, 0);
+    if (products) {
+      multiply(As, Bs, sx, sw0, sw1, acc, wn, wt, lane, load);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) load(j);
+    }
   }
 };
 
-template <int FA, int FB, int WN, int WT, int MODE>
+template <int FA, int FB, int WN, int WT, int MODE, int STAGES>
 __global__ __launch_bounds__(64 * WN * WT) void k_dense_fp8(const DenseArgs a) {
-  using D = Tile<FA, FB, WN, WT, MODE>;
+  using D = Tile<FA, FB, WN, WT, MODE, STAGES>;
   constexpr int TN = D::TN, TT = D::TT;
   constexpr bool GATED = D::GATED;
-  __shared__ __align__(16) uint8_t As0[TN * kStep], As1[TN * kStep];
-  __shared__ __align__(16) uint8_t Bs0[TT * kStep], Bs1[TT * kStep];
-  __shared__ __align__(16) float sxs[2][kScaleSteps][D::kSets * TT];  // xs * ws
+  __shared__ __align__(16) uint8_t As[STAGES * TN * kStep], Bs[STAGES * TT * kStep];
+  __shared__ __align__(16) float sxs[2 * TT * kScaleSteps];  // two runs of [token][step]
+  __shared__ float part[GATED ? WN : 1][GATED ? TT : 1];  // largest |H| of a token in a wave's columns
 
   int nt, tt;
   tile_of(a, nt, tt);
@@ -242,115 +284,134 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_fp8(const DenseArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave % WN, wt = wave / WN;
 
-  // Rows past the end lie past num_records: their loads return zeros.
-  const rsrc_t ra = make_rsrc(a.w + (int64_t)n0 * K, (uint32_t)n_live * K);
-  const rsrc_t ru = GATED ? make_rsrc(a.w + ((int64_t)a.N + n0) * K, (uint32_t)n_live * K) : ra;
-  const rsrc_t rb = make_rsrc(a.x + t0 * K, (uint32_t)t_live * K);
-  const rsrc_t rs = make_rsrc(a.xs + t0 * nb, (uint32_t)t_live * nb * 4);
-
-  // byte offsets of this lane's 16-byte pieces, K step 0; chunk: its logical position in the row
-  int va[D::kLoadsA], vb[D::kLoadsB], ca[D::kLoadsA], cb[D::kLoadsB];
+  typename D::Source src;
+  src.w = make_rsrc(a.w + (int64_t)n0 * K, (uint32_t)n_live * K);
+  src.up = GATED ? make_rsrc(a.w + ((int64_t)a.N + n0) * K, (uint32_t)n_live * K) : src.w;
+  src.x = make_rsrc(a.x + t0 * K, (uint32_t)t_live * K);
+  src.xs = make_rsrc(a.xs + t0 * nb, (uint32_t)t_live * nb * 4);
+  int cw[D::kLoadsA], cx[D::kLoadsB];  // the pieces' places within the step
 #pragma unroll
   for (int j = 0; j < D::kLoadsA; ++j) {
     const int r = 8 * (wave * D::kLoadsA + j) + (lane >> 3);
     const int row = GATED ? D::gated_col(r) : r;
-    ca[j] = ((lane & 7) ^ swz(r)) << 4;
-    va[j] = row < n_live ? row * K + ca[j] : kOutOfRange;
+    cw[j] = ((lane & 7) ^ swz(r)) << 4;
+    src.vw[j] = row < n_live ? row * K + cw[j] : kOutOfRange;
   }
 #pragma unroll
   for (int j = 0; j < D::kLoadsB; ++j) {
     const int r = 8 * (wave * D::kLoadsB + j) + (lane >> 3);
-    cb[j] = ((lane & 7) ^ swz(r)) << 4;
-    vb[j] = r < t_live ? r * K + cb[j] : kOutOfRange;
+    cx[j] = ((lane & 7) ^ swz(r)) << 4;
+    src.vx[j] = r < t_live ? r * K + cx[j] : kOutOfRange;
   }
-  // the last step of a ragged K: chunks past the row's end read as zeros
+  // the last step of a ragged K: chunks past the row's end read as zeros; past
+  // the last step nothing is read (the zeros go to buffers no step uses)
   const int tail = K % kStep ? K % kStep : kStep;
   auto cut = [&](int step) {
-    if (step == nb - 1 && tail < kStep) {
+    const int end = step >= nb ? 0 : step == nb - 1 ? tail : kStep;
+    if (end < kStep) {
 #pragma unroll
       for (int j = 0; j < D::kLoadsA; ++j)
-        if (ca[j] >= tail) va[j] = kOutOfRange;
+        if (cw[j] >= end) src.vw[j] = kOutOfRange;
 #pragma unroll
       for (int j = 0; j < D::kLoadsB; ++j)
-        if (cb[j] >= tail) vb[j] = kOutOfRange;
+        if (cx[j] >= end) src.vx[j] = kOutOfRange;
     }
   };
 
-  // Scales: the products xs ws of kScaleSteps steps are staged at a time.
-  // Thread -> (token, run of steps), and the kSets weight blocks of each step.
-  constexpr int V = D::kScalesPerThread, S = D::kSets;
-  const int s_tok = tid % TT, s_step = tid / TT * V;
+  // Activation scales: a run of kScaleSteps steps at a time, one direct load
+  // for 64 tokens (a lane takes its token's 16 bytes; those past the row's end
+  // belong to no step).  Weight scales: one for the wave's rows and step
+  // (gated: one of the gate rows, one of the up rows), a step ahead in scalar
+  // registers.  (Scales that pass through vector registers make the compiler
+  // wait for every load in flight.)
+  src.vs = (wave * 64 + lane) * nb * 4;
   const int nbn = (a.N + kFp8Block - 1) / kFp8Block;
-  const int w_blk = n0 / kFp8Block;
-  const rsrc_t rw = make_rsrc(a.ws, (uint32_t)((GATED ? 2 : 1) * nbn * nb) * 4u);
-  float sreg[V], wreg[S][V];
-  auto scales_load = [&](int kb) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int b = kb + s_step + i;
-      sreg[i] = __builtin_bit_cast(float, buf_u32(rs, b < nb ? (s_tok * nb + b) * 4 : kOutOfRange, 0));
-#pragma unroll
-      for (int q = 0; q < S; ++q) {
-        const int blk = GATED ? w_blk + q * nbn : min(w_blk + q, nbn - 1);
-        wreg[q][i] = __builtin_bit_cast(float, buf_u32(rw, b < nb ? (blk * nb + b) * 4 : kOutOfRange, 0));
-      }
-    }
-  };
-  auto scales_store = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int q = 0; q < S; ++q) sxs[buf][s_step + i][q * TT + s_tok] = sreg[i] * wreg[q][i];
-  };
+  const int blk = GATED ? n0 / kFp8Block : min((n0 + wn * 16 * FA) / kFp8Block, nbn - 1);
+  typedef const __attribute__((address_space(4))) float* const_floats;
+  const const_floats ws0 = (const_floats)(a.ws + (int64_t)blk * nb);
+  const const_floats ws1 = (const_floats)(a.ws + (int64_t)(blk + (GATED ? nbn : 0)) * nb);
 
+  // Round s loads step s + kAhead and multiplies step s; the first rounds only
+  // load.  A run's scales are loaded in the first round of the run before it
+  // (run 0's in the first round of all).
+  constexpr int kAhead = STAGES - 1;
   v4f acc[FA][FB] = {};
-  scales_load(0);
-  cut(0);
-  D::load_tiles(ra, ru, rb, As0, Bs0, va, vb, 0, wave);
-  scales_store(0);
-  for (int s = 0; s < nb; s += 2) {
-    const int sbuf = (s / kScaleSteps) & 1, srow = s % kScaleSteps;
-    loads_done_barrier();
-    // the next run's scales: loaded in a run's first step, stored in its second
-    if (srow == 0) scales_load(s + kScaleSteps);
-    cut(s + 1);
-    D::step(s + 1 < nb, ra, ru, rb, As0, Bs0, As1, Bs1, sxs[sbuf][srow], va, vb, (s + 1) * kStep, acc, wave, wn, wt,
+  int cur = 0, next = 0;  // buffers of the step multiplied, and of the step loaded
+  float sw0 = ws0[0], sw1 = ws1[0];
+#pragma unroll 1
+  for (int s = -kAhead; s < nb; ++s) {
+    // this step's tiles have landed (later ones may be on their way), and
+    // every wave has left the step whose buffers are loaded now
+    loads_done_barrier<(kAhead - 1) * D::kLoads>();
+    cut(s + kAhead);
+    const int run = s >> kScaleShift, at = s & (kScaleSteps - 1), later = s < 0 ? 0 : run + 1;
+    const bool scales = (at == 0 || s == -kAhead) && wave < TT / 64 && later * kScaleSteps < nb;
+    const int ahead = max(0, min(s + 1, nb - 1));
+    const float sw0_next = ws0[ahead], sw1_next = ws1[ahead];
+    D::step(s >= 0, src, (s + kAhead) * kStep, scales ? later * kScaleSteps * 4 : -1, As + cur * TN * kStep,
+            Bs + cur * TT * kStep, sxs + (run & 1) * TT * kScaleSteps + at, As + next * TN * kStep,
+            Bs + next * TT * kStep, sxs + ((later & 1) * TT + wave * 64) * kScaleSteps, sw0, sw1, acc, wave, wn, wt,
             lane);
-    if (s + 1 == nb) break;
-    loads_done_barrier();
-    if (srow == 0) scales_store(sbuf ^ 1);
-    cut(s + 2);
-    D::step(s + 2 < nb, ra, ru, rb, As1, Bs1, As0, Bs0, sxs[sbuf][srow + 1], va, vb, (s + 2) * kStep, acc, wave, wn, wt,
-            lane);
+    sw0 = sw0_next;
+    sw1 = sw1_next;
+    if (s >= 0) cur = cur + 1 == STAGES ? 0 : cur + 1;
+    next = next + 1 == STAGES ? 0 : next + 1;
   }
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no load may still write LDS when the workgroup ends
 
   const int r = lane & 15, g = lane >> 4;
   if constexpr (!GATED) {
-    const bool vec = a.N % 4 == 0;
+    const bool vec4 = a.N % 4 == 0, vec8 = a.N % 8 == 0;
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
       const int tl = wt * 16 * FB + 16 * j + r;
       const bool live = tl < t_live;
       const int64_t t = t0 + tl;
+      if (a.y_f32) {
 #pragma unroll
-      for (int i = 0; i < FA; ++i) {
-        const int n = n0 + wn * 16 * FA + 16 * i + 4 * g;
-        const v4f v = acc[i][j];
-        if (live && n < a.N) {
-          if (a.y_f32) {
+        for (int i = 0; i < FA; ++i) {
+          const int n = n0 + wn * 16 * FA + 16 * i + 4 * g;
+          const v4f v = acc[i][j];
+          if (live && n < a.N) {
             float* dst = a.y_f32 + t * a.N + n;
-            if (vec) *reinterpret_cast<v4f*>(dst) = v;
+            if (vec4) *reinterpret_cast<v4f*>(dst) = v;
             else
               for (int e = 0; e < 4; ++e)
                 if (n + e < a.N) dst[e] = v[e];
           }
-          if (a.y_bf16) {
-            uint16_t* dst = a.y_bf16 + t * a.N + n;
-            const uint2 pk = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-            if (vec) *reinterpret_cast<uint2*>(dst) = pk;
-            else
-              for (int e = 0; e < 4; ++e)
-                if (n + e < a.N) dst[e] = (uint16_t)((e < 2 ? pk.x : pk.y) >> (16 * (e & 1)));
+        }
+      }
+      if (a.y_bf16) {
+        // four fragments at a time (a narrow tile has two, and the other half
+        // of the lanes nothing to store), transposed among the lane groups: a
+        // lane then stores 16 neighbouring columns
+#pragma unroll
+        for (int q = 0; q < FA; q += 4) {
+          uint32_t lo[4], hi[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const v4f v = acc[q + i < FA ? q + i : q][j];
+            lo[i] = pack_bf16(v[0], v[1]);
+            hi[i] = pack_bf16(v[2], v[3]);
+          }
+          transpose4(lo);
+          transpose4(hi);
+          const int n = n0 + wn * 16 * FA + 16 * (q + g);
+          uint16_t* dst = a.y_bf16 + t * a.N + n;
+          if (!live || q + g >= FA) continue;
+          if (vec8) {
+            if (n < a.N) *reinterpret_cast<uint4*>(dst) = uint4{lo[0], hi[0], lo[1], hi[1]};
+            if (n + 8 < a.N) *reinterpret_cast<uint4*>(dst + 8) = uint4{lo[2], hi[2], lo[3], hi[3]};
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (vec4) {
+                if (n + 4 * i < a.N) *reinterpret_cast<uint2*>(dst + 4 * i) = uint2{lo[i], hi[i]};
+              } else {
+                for (int e = 0; e < 4; ++e)
+                  if (n + 4 * i + e < a.N) dst[4 * i + e] = (uint16_t)((e < 2 ? lo[i] : hi[i]) >> (16 * (e & 1)));
+              }
+            }
           }
         }
       }
@@ -391,7 +452,6 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_fp8(const DenseArgs a) {
   } else {
     // H = silu(G) U in place of the gate accumulators; a token's 128 columns
     // of the tile are one e4m3 block, held by WN waves
-    __shared__ float part[WN][TT];
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
       float amax = 0.f;
@@ -408,7 +468,7 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_fp8(const DenseArgs a) {
       amax = fmaxf(amax, __shfl_xor(amax, 32));
       if (g == 0) part[wn][wt * 16 * FB + 16 * j + r] = amax;
     }
-    __syncthreads();
+    lds_barrier();
     const int hb = (a.N + kFp8Block - 1) / kFp8Block;
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
@@ -420,29 +480,75 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_fp8(const DenseArgs a) {
       float id;
       const float scale = fp8_scale(amax, id);
       const int64_t t = t0 + tl;
-      if (tl < t_live) {
-        if (wn == 0 && g == 0) a.hs[t * hb + n0 / kFp8Block] = scale;
+      if (tl < t_live && wn == 0 && g == 0) a.hs[t * hb + n0 / kFp8Block] = scale;
+      uint32_t pk[FA / 2];
+#pragma unroll
+      for (int i = 0; i < FA / 2; ++i) {
+        const v4f v = acc[i][j];
+        pk[i] = pack_e4m3(v[0] * id, v[1] * id, v[2] * id, v[3] * id);
+      }
+      if constexpr (FA == 8) {  // a lane stores 16 neighbouring columns
+        transpose4(pk);
+        const int n = wn * 64 + 16 * g;
+        if (tl < t_live && n < n_live)
+          *reinterpret_cast<uint4*>(a.h + t * a.N + n0 + n) = uint4{pk[0], pk[1], pk[2], pk[3]};
+      } else {
 #pragma unroll
         for (int i = 0; i < FA / 2; ++i) {
           const int n = wn * 8 * FA + 16 * i + 4 * g;
-          const v4f v = acc[i][j];
-          if (n < n_live)
-            *reinterpret_cast<uint32_t*>(a.h + t * a.N + n0 + n) = pack_e4m3(v[0] * id, v[1] * id, v[2] * id, v[3] * id);
+          if (tl < t_live && n < n_live) *reinterpret_cast<uint32_t*>(a.h + t * a.N + n0 + n) = pk[i];
         }
       }
     }
   }
 }
 
-template <int FA, int FB, int WN, int WT, int MODE>
+template <int FA, int FB, int WN, int WT, int MODE, int STAGES>
 hipError_t run(DenseArgs a, hipStream_t st) {
-  using D = Tile<FA, FB, WN, WT, MODE>;
+  using D = Tile<FA, FB, WN, WT, MODE, STAGES>;
   const int tn = MODE == kGated ? D::TN / 2 : D::TN;
   a.n_nt = (a.N + tn - 1) / tn;
   a.n_tt = (int)((a.T + D::TT - 1) / D::TT);
-  hipLaunchKernelGGL((k_dense_fp8<FA, FB, WN, WT, MODE>), dim3((unsigned)(a.n_nt * a.n_tt)), dim3(D::kThreads), 0, st,
-                     a);
+  hipLaunchKernelGGL((k_dense_fp8<FA, FB, WN, WT, MODE, STAGES>), dim3((unsigned)(a.n_nt * a.n_tt)), dim3(D::kThreads),
+                     0, st, a);
   return hipGetLastError();
+}
+
+// Choice of the tile.  Large tiles move fewer bytes through LDS for a product,
+// small ones fill the chip with few rows and leave less of its last pass idle.
+// The time of a variant is estimated from what one CU was measured to take for
+// a K step while it holds 1, 2, ... of the variant's tiles (us; the launch has
+// 256 CUs busy) and for what a tile costs beside its steps: passes with every
+// CU full, then one with the tiles that remain.
+struct Variant {
+  int cols, tokens;  // of a tile
+  int per_cu;        // tiles a CU holds (LDS)
+  float fixed, step[4];
+};
+constexpr Variant kFastTiles[] = {{256, 256, 1, 9.f, {1.68f}},
+                                  {128, 128, 2, 6.f, {0.84f, 1.02f}},
+                                  {128, 64, 3, 5.f, {0.62f, 0.74f, 0.93f}},
+                                  {64, 64, 4, 4.f, {0.45f, 0.60f, 0.71f, 0.79f}}};
+constexpr Variant kExactTiles[] = {{128, 128, 2, 7.f, {1.04f, 1.73f}},
+                                   {128, 64, 3, 6.f, {0.72f, 1.09f, 1.50f}},
+                                   {64, 64, 4, 5.f, {0.55f, 0.69f, 0.95f, 1.22f}}};
+constexpr Variant kGatedTiles[] = {{128, 256, 1, 9.f, {1.62f}}, {128, 128, 1, 9.f, {0.95f}}, {128, 64, 1, 6.f, {0.65f}}};
+
+template <int COUNT>
+int pick(const Variant (&v)[COUNT], int64_t T, int N, int nb, int num_cus) {
+  int best = 0;
+  float least = 0.f;
+  for (int i = 0; i < COUNT; ++i) {
+    const int64_t tiles = ((T + v[i].tokens - 1) / v[i].tokens) * ((N + v[i].cols - 1) / v[i].cols);
+    const int64_t slots = (int64_t)num_cus * v[i].per_cu, passes = tiles / slots, rest = tiles % slots;
+    float t = (float)passes * (v[i].step[v[i].per_cu - 1] * (float)nb + v[i].fixed);
+    if (rest) t += v[i].step[(rest + num_cus - 1) / num_cus - 1] * (float)nb + v[i].fixed;
+    if (i == 0 || t < least) {
+      best = i;
+      least = t;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -450,15 +556,29 @@ hipError_t run(DenseArgs a, hipStream_t st) {
 hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int64_t T, int N,
                             int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus, hipStream_t st) {
   const DenseArgs a{x, xs, w, ws, y_f32, y_bf16, y_q8, nullptr, nullptr, T, N, K, (K + kStep - 1) / kStep, 0, 0};
-  // fp32 outputs take the bf16 products (see the head of the file)
-  if (y_f32) return run<4, 4, 2, 2, kExact>(a, st);
-  return run<4, 4, 2, 2, kFast>(a, st);
+  if (y_f32) {  // exact products (see the head of the file)
+    switch (pick(kExactTiles, T, N, a.nb, num_cus)) {
+      case 0: return run<4, 4, 2, 2, kExact, 2>(a, st);
+      case 1: return run<4, 2, 2, 2, kExact, 2>(a, st);
+      default: return run<2, 2, 2, 2, kExact, 2>(a, st);
+    }
+  }
+  switch (pick(kFastTiles, T, N, a.nb, num_cus)) {
+    case 0: return run<8, 4, 2, 4, kFast, 2>(a, st);
+    case 1: return run<4, 4, 2, 2, kFast, 2>(a, st);
+    case 2: return run<4, 2, 2, 2, kFast, 2>(a, st);
+    default: return run<2, 2, 2, 2, kFast, 2>(a, st);
+  }
 }
 
 hipError_t launch_gateup_fp8(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int64_t T, int F,
                              int C, uint8_t* h, float* hs, int num_cus, hipStream_t st) {
   const DenseArgs a{x, xs, gu, gus, nullptr, nullptr, nullptr, h, hs, T, F, C, (C + kStep - 1) / kStep, 0, 0};
-  return run<8, 4, 2, 1, kGated>(a, st);
+  switch (pick(kGatedTiles, T, F, a.nb, num_cus)) {
+    case 0: return run<8, 4, 2, 4, kGated, 2>(a, st);
+    case 1: return run<4, 4, 4, 2, kGated, 3>(a, st);
+    default: return run<8, 2, 2, 2, kGated, 3>(a, st);
+  }
 }
 
 }  // namespace latmoe
