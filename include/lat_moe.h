@@ -354,8 +354,8 @@ int lat_moe_dense_fp8(const void* x_fp8, const float* x_scales, const void* w_fp
  *                    lat_moe_ffn_fp8_workspace_size(T, C, F); its contents need
  *                    no initialisation
  * Supported: T >= 0, T < 2^31, C % 16 == 0, F % 16 == 0, 16 <= C, F <= 65536,
- * and at most 2^31 tiles of each product as above (the size is 0 for
- * unsupported shapes).  Pointers 16-byte aligned.  T = 0 enqueues nothing.
+ * 2F * C < 2^31, and at most 2^31 tiles of each product as above (the size is 0
+ * for unsupported shapes).  Pointers 16-byte aligned.  T = 0 enqueues nothing.
  * Outputs are deterministic. */
 size_t lat_moe_ffn_fp8_workspace_size(int64_t T, int32_t C, int32_t F);
 int lat_moe_ffn_fp8(const void* x_fp8, const float* x_scales, const void* gateup_fp8, const float* gateup_scales,

@@ -222,7 +222,8 @@ hipError_t dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const 
 }
 
 bool ffn_fp8_ok(int64_t T, int32_t C, int32_t F) {
-  return fp8_dense_ok(T, F, C) && fp8_dense_ok(T, C, F) && ((T + 63) / 64) * ((F + 31) / 32) < (int64_t)1 << 31;
+  // the gate/up matrix below 2 GiB (32-bit offsets)
+  return fp8_dense_ok(T, F, C) && fp8_dense_ok(T, C, F) && fp8_cols_ok(F) && (int64_t)2 * F * C < (int64_t)1 << 31;
 }
 // Workspace of the gated block: H's codes and scales, and for few tokens the
 // fp32 H that they are rounded from.
@@ -369,7 +370,7 @@ int lat_moe_rmsnorm(const void* x, int32_t x_type, const void* residual, int32_t
   int rc = check_device(&num_cus);
   if (rc != LAT_MOE_OK) return rc;
   const NormArgs a{x, residual, weight, residual_out, y, static_cast<uint8_t*>(y_q8_1), static_cast<uint8_t*>(y_fp8),
-                   y_scales, T, C, x_type, residual_type, y_type, eps};
+                   y_scales, T, C, x_type, residual_type, y_type, eps, 1.0 / C};
   if (launch_rmsnorm(a, num_cus, static_cast<hipStream_t>(stream)) != hipSuccess) return LAT_MOE_ELAUNCH;
   return LAT_MOE_OK;
 }
@@ -423,9 +424,14 @@ int lat_moe_ffn_fp8(const void* x_fp8, const float* x_scales, const void* gateup
   float* hs = h_fp8 ? h_scales : reinterpret_cast<float*>(ws + L.scales);
   if (T <= kFp8SmallT) {
     float* h32 = reinterpret_cast<float*>(ws + L.h32);
-    if (launch_gateup_fp8_small(x, x_scales, gu, gateup_scales, (int)T, F, C, h32, st) != hipSuccess ||
-        launch_quantize_fp8(h32, LAT_MOE_F32, T, F, h, hs, st) != hipSuccess)
+    if (launch_gateup_fp8_small(x, x_scales, gu, gateup_scales, (int)T, F, C, h32, st) != hipSuccess)
       return LAT_MOE_ELAUNCH;
+    if (T <= kFp8RoundT && !h_fp8)  // H's codes are not asked for: the down projection rounds H as it reads it
+      return launch_dense_fp8_round(h32, static_cast<const uint8_t*>(down_fp8), down_scales, (int)T, C, F, y_f32,
+                                    static_cast<uint16_t*>(y_bf16), st) == hipSuccess
+                 ? LAT_MOE_OK
+                 : LAT_MOE_ELAUNCH;
+    if (launch_quantize_fp8(h32, LAT_MOE_F32, T, F, h, hs, st) != hipSuccess) return LAT_MOE_ELAUNCH;
   } else if (launch_gateup_fp8(x, x_scales, gu, gateup_scales, T, F, C, h, hs, num_cus, st) != hipSuccess) {
     return LAT_MOE_ELAUNCH;
   }

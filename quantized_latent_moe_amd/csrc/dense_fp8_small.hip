@@ -17,8 +17,9 @@ namespace {
 constexpr int kWaves = 8;
 
 struct SmallArgs {
-  const uint8_t* x;
+  const uint8_t* x;  // [T][K] e4m3, or null: the rows are h32
   const float* xs;
+  const float* h32;  // [T][K] fp32 rows to be rounded to e4m3 here
   const uint8_t* w;
   const float* ws;
   float* y_f32;
@@ -36,13 +37,22 @@ __device__ __forceinline__ void widen16(const uint4* p, v8bf* o) {
   }
 }
 
+// What a kernel computes: a projection of e4m3 rows; the gated pair (its 16
+// weight rows are 8 gate rows and the same columns' 8 up rows, so that one
+// fragment holds both and twice as many workgroups share the weights); a
+// projection of fp32 rows that it rounds to e4m3 itself (every workgroup
+// rounds them again, which for 16 tokens costs less than a launch between).
+enum SmallMode : int { kRows = 0, kGatedPair = 1, kRound = 2 };
+
 // Token columns past T and weight rows past N hold zeros or a clamped row;
 // they meet only results that are not stored.
-template <int FR, int TF, bool GATED>
+template <int FR, int TF, int MODE>
 __global__ __launch_bounds__(64 * kWaves) void k_dense_fp8_small(const SmallArgs a) {
-  constexpr int U = TF == 1 ? 4 : 2;  // blocks in flight per wave
-  constexpr int NF = GATED ? 16 : 16 * FR;  // output columns
-  static_assert(!GATED || FR == 2, "a gate fragment and its up fragment");
+  constexpr bool GATED = MODE == kGatedPair;
+  constexpr int U = MODE == kRound || TF > 1 ? 2 : 4;  // blocks in flight per wave
+  constexpr int NF = GATED ? 8 : 16 * FR;              // output columns
+  static_assert(!GATED || FR == 1, "one fragment of gate and up rows");
+  static_assert(MODE != kRound || TF == 1, "rounding for 16 tokens");
   __shared__ __align__(16) float red[kWaves][FR * TF][64][4];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -53,22 +63,29 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_fp8_small(const SmallArgs
   const int nbn = (a.N + kFp8Block - 1) / kFp8Block;
 
   rsrc_t rw[FR];
-  int wrow[FR], wblk[FR];
+  int wrow[FR], wblk[FR];  // byte offset of the lane's weight row; of the scales of the lane's result rows
 #pragma unroll
   for (int i = 0; i < FR; ++i) {
-    const int first = GATED ? n0 : n0 + 16 * i;  // of the fragment's 16 rows
-    const int base = min(first, a.N - 1);
-    rw[i] = make_rsrc(a.w + ((GATED && i ? (int64_t)a.N : 0) + base) * K, (uint32_t)min(16, a.N - base) * K);
-    wrow[i] = min(r, a.N - 1 - base) * K;
-    wblk[i] = ((GATED && i ? nbn : 0) + base / kFp8Block) * nb;
+    const int base = min(n0 + 16 * i, a.N - 1);  // of the fragment's rows
+    if (GATED) {
+      const int live = min(8, a.N - base);
+      rw[i] = make_rsrc(a.w + (int64_t)base * K, (uint32_t)(a.N + live) * (uint32_t)K);
+      wrow[i] = (min(r & 7, live - 1) + (r < 8 ? 0 : a.N)) * K;
+      wblk[i] = (base / kFp8Block + (g < 2 ? 0 : nbn)) * nb;
+    } else {
+      const int live = min(16, a.N - base);
+      rw[i] = make_rsrc(a.w + (int64_t)base * K, (uint32_t)live * K);
+      wrow[i] = min(r, live - 1) * K;
+      wblk[i] = base / kFp8Block * nb;
+    }
   }
-  const rsrc_t rx = make_rsrc(a.x, (uint32_t)a.T * K);
-  const rsrc_t rs = make_rsrc(a.xs, (uint32_t)a.T * nb * 4);
+  const rsrc_t rx = MODE == kRound ? make_rsrc(a.h32, (uint32_t)a.T * K * 4) : make_rsrc(a.x, (uint32_t)a.T * K);
+  const rsrc_t rs = MODE == kRound ? rx : make_rsrc(a.xs, (uint32_t)a.T * nb * 4);
   const rsrc_t rws = make_rsrc(a.ws, (uint32_t)((GATED ? 2 : 1) * nbn * nb) * 4u);
 
   v4f acc[FR][TF] = {};
   for (int k0 = wave; k0 < nb; k0 += U * kWaves) {
-    uint4 wa[U][FR][2], xa[U][TF][2];
+    uint4 wa[U][FR][2], xa[U][TF][2], xh[U][MODE == kRound ? 8 : 1];
     float sx[U][TF], sw[U][FR];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -81,16 +98,47 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_fp8_small(const SmallArgs
         wa[u][i][1] = buf_u128(rw[i], in1 ? wrow[i] + c1 : kOutOfRange, 0);
         sw[u][i] = __builtin_bit_cast(float, buf_u32(rws, kb < nb ? (wblk[i] + kb) * 4 : kOutOfRange, 0));
       }
+      if constexpr (MODE == kRound) {
 #pragma unroll
-      for (int j = 0; j < TF; ++j) {
-        const int t = 16 * j + r;
-        xa[u][j][0] = buf_u128(rx, in0 && t < a.T ? t * K + c0 : kOutOfRange, 0);
-        xa[u][j][1] = buf_u128(rx, in1 && t < a.T ? t * K + c1 : kOutOfRange, 0);
-        sx[u][j] = __builtin_bit_cast(float, buf_u32(rs, kb < nb && t < a.T ? (t * nb + kb) * 4 : kOutOfRange, 0));
+        for (int e = 0; e < 4; ++e) {
+          xh[u][e] = buf_u128(rx, in0 && r < a.T ? (r * K + c0 + 4 * e) * 4 : kOutOfRange, 0);
+          xh[u][4 + e] = buf_u128(rx, in1 && r < a.T ? (r * K + c1 + 4 * e) * 4 : kOutOfRange, 0);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < TF; ++j) {
+          const int t = 16 * j + r;
+          xa[u][j][0] = buf_u128(rx, in0 && t < a.T ? t * K + c0 : kOutOfRange, 0);
+          xa[u][j][1] = buf_u128(rx, in1 && t < a.T ? t * K + c1 : kOutOfRange, 0);
+          sx[u][j] = __builtin_bit_cast(float, buf_u32(rs, kb < nb && t < a.T ? (t * nb + kb) * 4 : kOutOfRange, 0));
+        }
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      if constexpr (MODE == kRound) {
+#pragma clang fp contract(off)
+        // the four lanes of token r hold its block of 128 values
+        float v[32], id;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t w[4] = {xh[u][e].x, xh[u][e].y, xh[u][e].z, xh[u][e].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[4 * e + i] = __builtin_bit_cast(float, w[i]);
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
+        amax = fmaxf(amax, __shfl_xor(amax, 16));
+        amax = fmaxf(amax, __shfl_xor(amax, 32));
+        sx[u][0] = fp8_scale(amax, id);
+        uint32_t pk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          pk[e] = pack_e4m3(v[4 * e] * id, v[4 * e + 1] * id, v[4 * e + 2] * id, v[4 * e + 3] * id);
+        xa[u][0][0] = uint4{pk[0], pk[1], pk[2], pk[3]};
+        xa[u][0][1] = uint4{pk[4], pk[5], pk[6], pk[7]};
+      }
 #pragma unroll
       for (int i = 0; i < FR; ++i) {
         v8bf fa[4];
@@ -107,6 +155,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_fp8_small(const SmallArgs
           for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(s, d[e], acc[i][j][e]);
         }
       }
+    }
   }
 #pragma unroll
   for (int i = 0; i < FR; ++i)
@@ -127,7 +176,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_fp8_small(const SmallArgs
     const bool live = t < a.T && n < a.N;  // a whole 32-column block of a token, or none of it, where N % 32 == 0
     float v = total(c, t);
     if constexpr (GATED) {
-      const float u = total(16 + c, t);
+      const float u = total(8 + c, t);
       v = v / (1.0f + __expf(-v)) * u;
     }
     if (live && a.y_f32) a.y_f32[(int64_t)t * a.N + n] = v;
@@ -157,28 +206,40 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_fp8_small(const SmallArgs
   }
 }
 
-template <int FR, bool GATED>
+template <int FR, int MODE>
 void run(const SmallArgs& a, hipStream_t st) {
-  const int nf = GATED ? 16 : 16 * FR;
+  const int nf = MODE == kGatedPair ? 8 : 16 * FR;
   const dim3 grid((unsigned)((a.N + nf - 1) / nf)), block(64 * kWaves);
-  if (a.T <= 16) hipLaunchKernelGGL((k_dense_fp8_small<FR, 1, GATED>), grid, block, 0, st, a);
-  else if (a.T <= 32) hipLaunchKernelGGL((k_dense_fp8_small<FR, 2, GATED>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_dense_fp8_small<FR, 4, GATED>), grid, block, 0, st, a);
+  if constexpr (MODE == kRound) {
+    hipLaunchKernelGGL((k_dense_fp8_small<FR, 1, MODE>), grid, block, 0, st, a);
+  } else {
+    if (a.T <= 16) hipLaunchKernelGGL((k_dense_fp8_small<FR, 1, MODE>), grid, block, 0, st, a);
+    else if (a.T <= 32) hipLaunchKernelGGL((k_dense_fp8_small<FR, 2, MODE>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_dense_fp8_small<FR, 4, MODE>), grid, block, 0, st, a);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_dense_fp8_small(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int T, int N,
                                   int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, hipStream_t st) {
-  const SmallArgs a{x, xs, w, ws, y_f32, y_bf16, y_q8, T, N, K, (K + kFp8Block - 1) / kFp8Block};
-  if (y_q8) run<2, false>(a, st);  // a q8_1 block is 32 columns
-  else run<1, false>(a, st);
+  const SmallArgs a{x, xs, nullptr, w, ws, y_f32, y_bf16, y_q8, T, N, K, (K + kFp8Block - 1) / kFp8Block};
+  if (y_q8) run<2, kRows>(a, st);  // a q8_1 block is 32 columns
+  else run<1, kRows>(a, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_dense_fp8_round(const float* h, const uint8_t* w, const float* ws, int T, int N, int K, float* y_f32,
+                                  uint16_t* y_bf16, hipStream_t st) {
+  run<1, kRound>(SmallArgs{nullptr, nullptr, h, w, ws, y_f32, y_bf16, nullptr, T, N, K,
+                           (K + kFp8Block - 1) / kFp8Block}, st);
   return hipGetLastError();
 }
 
 hipError_t launch_gateup_fp8_small(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int T,
                                    int F, int C, float* h, hipStream_t st) {
-  run<2, true>(SmallArgs{x, xs, gu, gus, h, nullptr, nullptr, T, F, C, (C + kFp8Block - 1) / kFp8Block}, st);
+  run<1, kGatedPair>(SmallArgs{x, xs, nullptr, gu, gus, h, nullptr, nullptr, T, F, C,
+                               (C + kFp8Block - 1) / kFp8Block}, st);
   return hipGetLastError();
 }
 

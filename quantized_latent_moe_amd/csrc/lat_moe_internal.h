@@ -249,6 +249,7 @@ struct NormArgs {
   int64_t T;
   int C, x_type, residual_type, y_type;
   float eps;
+  double inv_c;  // 1 / C
 };
 hipError_t launch_rmsnorm(const NormArgs& a, int num_cus, hipStream_t st);
 // e4m3 rows [T][K] x e4m3 weights [N][K] -> y in fp32, bf16 and/or q8_1 (any may be null, not all).
@@ -258,6 +259,10 @@ hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w,
 constexpr int kFp8SmallT = 64;
 hipError_t launch_dense_fp8_small(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int T, int N,
                                   int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, hipStream_t st);
+// fp32 rows h [T][K] of at most kFp8RoundT tokens, rounded to e4m3 rows on the way, x e4m3 weights.
+constexpr int kFp8RoundT = 16;
+hipError_t launch_dense_fp8_round(const float* h, const uint8_t* w, const float* ws, int T, int N, int K, float* y_f32,
+                                  uint16_t* y_bf16, hipStream_t st);
 // silu(G) * U of at most kFp8SmallT tokens, unrounded: h [T][F] fp32.
 hipError_t launch_gateup_fp8_small(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int T,
                                    int F, int C, float* h, hipStream_t st);

@@ -18,6 +18,18 @@ __device__ __forceinline__ double wave_sum(double s) {
   return s;
 }
 
+// 1 / sqrt(a), a > 0, rounded to fp32: the hardware's 64-bit estimate (at least
+// 20 bits) and two steps of y += y (1 - a y^2) / 2, each of which doubles them.
+__device__ __forceinline__ float inverse_root(double a) {
+  double y = __builtin_amdgcn_rsq(a);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const double e = __builtin_fma(-a * y, y, 1.0);
+    y = __builtin_fma(0.5 * y, e, y);
+  }
+  return (float)y;
+}
+
 // Adds CH chunks of residual (TYPE) to v.
 template <int TYPE, int TPR, int CH>
 __device__ __forceinline__ void add_rows(const void* p, int64_t row, int lane, int C, float (*v)[8]) {
@@ -52,6 +64,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(const NormArg
   const int C = a.C;
   const int64_t row = t * C;
   float v[CH][8];
+  // the weights are on their way during the sum, where the registers allow it
+  constexpr bool kEarly = CH <= 2;
+  Raw8<LAT_MOE_F32> weight[kEarly ? CH : 1];
   {
     Raw8<XT> raw[CH];
 #pragma unroll
@@ -59,6 +74,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(const NormArg
       const int c = (i * TPR + lane) * 8;
       if (c < C) raw[i].load(a.x, row + c);
       else raw[i].zero();
+    }
+    if constexpr (kEarly) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = (i * TPR + lane) * 8;
+        if (c < C) weight[i].load(a.weight, c);
+        else weight[i].zero();
+      }
     }
 #pragma unroll
     for (int i = 0; i < CH; ++i) raw[i].values(v[i]);
@@ -84,7 +107,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(const NormArg
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) ss += part[w];
   }
-  const float r = (float)(1.0 / __builtin_sqrt(ss / C + (double)a.eps));
+  const float r = inverse_root(ss * a.inv_c + (double)a.eps);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = (i * TPR + lane) * 8;
@@ -93,9 +116,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(const NormArg
     float y[8];
     if (in) {
       float g[8];
-      Raw8<LAT_MOE_F32> w;
-      w.load(a.weight, c);
-      w.values(g);
+      if constexpr (kEarly) {
+        weight[i].values(g);
+      } else {
+        Raw8<LAT_MOE_F32> w;
+        w.load(a.weight, c);
+        w.values(g);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] = v[i][j] * r * g[j];
     } else {

@@ -64,7 +64,7 @@ def test_dense_fp8_refusals():
 def test_ffn_fp8_refusals_and_workspace():
     size = lm.ffn_fp8_workspace_size
     for T, C, F in [(-1, 64, 64), (4, 8, 64), (4, 64, 8), (4, 72, 64), (4, 64, 72), (4, 65552, 64), (4, 64, 65552),
-                    (1 << 31, 64, 64), (4, 1 << 32, 64), ((1 << 31) - 1, 64, 65536)]:
+                    (1 << 31, 64, 64), (4, 1 << 32, 64), ((1 << 31) - 1, 64, 65536), (4, 32768, 32768)]:
         assert size(T, C, F) == 0, (T, C, F)
     for T, C, F in [(0, 64, 64), (1, 64, 64), (64, 512, 1040), (65, 512, 1040), (5268, 4096, 8192)]:
         assert size(T, C, F) >= max(1, T * F + 4 * T * -(-F // 128)), (T, C, F)
