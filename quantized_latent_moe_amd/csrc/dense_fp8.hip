@@ -21,12 +21,21 @@
 //
 // One workgroup computes TN = 16 FA WN weight rows x TT = 16 FB WT tokens.
 // Weights are the MFMA's row operand: a lane then holds four neighbouring
-// weight rows of one token, one scale for a whole MFMA result, and stores
-// four neighbouring outputs at once.  Per K step of 128 both tiles go to LDS
-// by direct loads (16 bytes a lane, no registers), double-buffered; a row is
-// 128 bytes, its 16-byte chunks XOR-swizzled by the row so that a fragment
-// read touches every bank once (the swizzle is applied to the global address
-// of a lane, since the LDS side of a direct load is linear).
+// weight rows of one token, one scale for a whole MFMA result.  NP waves only
+// load: per K step of 128 both tiles go to LDS by direct loads (16 bytes a
+// lane, no registers), STAGES steps ahead; a row is 128 bytes, its 16-byte
+// chunks XOR-swizzled by the row so that a fragment read touches every bank
+// once (the swizzle is applied to the global address of a lane, since the LDS
+// side of a direct load is linear).  WN x WT waves multiply: each reads its
+// fragments a step ahead into the registers that their last MFMA has left, so
+// that no LDS latency stands between two steps, and one barrier a step joins
+// all waves.  (A wave that loads and multiplies waits for the memory pipe to
+// take each load, 20 cycles for each of all the waves' loads, and its MFMAs
+// with it: 128 x 128 tiles took 0.7 us a step that way and take 0.47 us now.)
+//
+// What bounds it: direct loads reach about 100 GB/s a CU, 0.48 us for a step
+// of 256 x 128, and the MFMAs of that step take 0.5 to 0.57 us (the clock
+// falls to 1.8 GHz under them); together, with the LDS reads between, 0.87 us.
 #include <type_traits>
 
 #include "block_fp8.h"
@@ -106,17 +115,17 @@ __device__ __forceinline__ void tile_of(const DenseArgs& a, int& nt, int& tt) {
 // projection with bf16 products, or the gated pair of projections.
 enum Mode : int { kFast = 0, kExact = 1, kGated = 2 };
 
-template <int FA, int FB, int WN, int WT, int MODE, int STAGES>
+template <int FA, int FB, int WN, int WT, int MODE, int STAGES, int NP>
 struct Tile {
   static constexpr bool GATED = MODE == kGated;
-  static constexpr int kThreads = 64 * WN * WT;
+  static constexpr int kWaves = WN * WT;                // that multiply; NP more load
+  static constexpr int kThreads = 64 * (kWaves + NP);
   static constexpr int TN = 16 * FA * WN, TT = 16 * FB * WT;
-  static constexpr int kWaves = WN * WT;
-  static constexpr int kLoadsA = TN / 8 / kWaves, kLoadsB = TT / 8 / kWaves;  // 1 KB each
+  static constexpr int kLoadsA = TN / 8 / NP, kLoadsB = TT / 8 / NP;  // 1 KB each
   static_assert(kFp8Block % (16 * FA) == 0, "a wave's weight rows lie in one scale block");
-  static_assert(TN % (8 * kWaves) == 0 && TT % (8 * kWaves) == 0, "whole loads");
-  static_assert(TT % 64 == 0 && TT / 64 <= kWaves, "a wave loads 64 tokens' scales");
-  static_assert(STAGES == 2 || STAGES == 3, "one or two steps ahead");
+  static_assert(TN % (8 * NP) == 0 && TT % (8 * NP) == 0, "whole loads");
+  static_assert(TT % 64 == 0, "a load takes 64 tokens' scales");
+  static_assert(STAGES >= 2, "at least a step ahead");
   static_assert(!GATED || TN == 256, "a gated tile holds one e4m3 block of H");
 
   // H column (within the tile) of LDS row r of the weight tile, gated tiles:
@@ -134,7 +143,7 @@ struct Tile {
   // K step 0.  Only the step's start, in the scalar offset, changes.
   struct Source {
     rsrc_t w, up, x, xs;
-    int vw[kLoadsA], vx[kLoadsB], vs;
+    int vw[kLoadsA], vx[kLoadsB];
   };
   // The wave's j-th direct load of a K step into LDS: weight rows, then tokens.
   static constexpr int kLoads = kLoadsA + kLoadsB;
@@ -151,13 +160,21 @@ struct Tile {
     }
   }
 
-  static __device__ __forceinline__ v8i fragment(const uint8_t* s, int row, int g) {
-    // chunks g and g + 4 of the row: the same K order in both operands, and no
-    // two of the lanes that LDS serves together meet in a bank (chunks 2g and
-    // 2g + 1 with this swizzle do, at half the read rate)
-    const v4i lo = *reinterpret_cast<const v4i*>(s + row * kStep + ((g ^ swz(row)) << 4));
-    const v4i hi = *reinterpret_cast<const v4i*>(s + row * kStep + (((g + 4) ^ swz(row)) << 4));
-    return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  static __device__ __forceinline__ void load_16(rsrc_t r, void* lds, int v) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, v, 0, 0, 0);
+  }
+
+  // LDS offset of chunk g of lane (r, g)'s row in a tile's first fragment.
+  // Chunks g and g + 4 make the operand (64 bytes apart, whatever the swizzle):
+  // the same K order on both sides, and no two of the lanes that LDS serves
+  // together meet in a bank (chunks 2g and 2g + 1 with this swizzle do, at
+  // half the read rate).
+  static __device__ __forceinline__ int lane_offset(int row, int g) { return row * kStep + ((g ^ swz(row)) << 4); }
+  // Fragment i from the lane's two chunk addresses (16 rows are 2 KB).
+  static __device__ __forceinline__ v8i fragment(const uint8_t* lo, const uint8_t* hi, int i) {
+    const v4i l = *reinterpret_cast<const v4i*>(lo + i * 16 * kStep);
+    const v4i h = *reinterpret_cast<const v4i*>(hi + i * 16 * kStep);
+    return v8i{l[0], l[1], l[2], l[3], h[0], h[1], h[2], h[3]};
   }
 
   // An MFMA operand of 16 rows and K = 128: the e4m3 codes, or (kExact) the
@@ -186,87 +203,71 @@ struct Tile {
     return p;
   }
 
-  // The step's products, and the direct loads of a later one.  The MFMA of
-  // fragment pair q is issued before the fold of pair q - kLag, whose result
-  // is then complete; weight fragments are read two rows of pairs ahead, and
-  // the loads are spread over the pairs (issued together at the step's start
-  // they hold the wave back until the memory pipe has taken them).
-  static constexpr int kLag = 4;
-  template <class Load>
-  static __device__ __forceinline__ void multiply(const uint8_t* As, const uint8_t* Bs, const float* sx, float sw0,
-                                                  float sw1, v4f (*acc)[FB], int wn, int wt, int lane, Load load) {
-    const int r = lane & 15, g = lane >> 4;
-    const int a_row = wn * 16 * FA + r, b_row = wt * 16 * FB + r;
-    v8i a[3], bf[FB];
-    Operand ao, b[FB];
-    float s[GATED ? 2 : 1][FB];
-    a[0] = fragment(As, a_row, g);
-#pragma unroll
-    for (int j = 0; j < FB; ++j) bf[j] = fragment(Bs, b_row + 16 * j, g);
-    a[1] = fragment(As, a_row + 16, g);
+  // What a multiplying wave carries from step to step: the fragments and
+  // scales of the step in hand, and the results that are not folded yet.
+  static constexpr int kLag = 3;  // an MFMA's result is folded three MFMAs later
+  static constexpr int kSides = GATED ? 2 : 1;
+  static_assert(FA * FB % (kLag + 1) == 0, "the results' registers come round with the step");
+  struct State {
+    v8i a[FA], b[FB];
+    float s[kSides][FB], s_last[kSides][FB];  // of this step, and of the one before
+    v4f p[kLag + 1];
+  };
+  static __device__ __forceinline__ void scales(State& st, const float* sx, float sw0, float sw1) {
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
-      const float x = sx[(b_row + 16 * j) * kScaleSteps];
-      s[0][j] = x * sw0;
-      if (GATED) s[GATED][j] = x * sw1;
+      const float x = sx[16 * j * kScaleSteps];
+      st.s[0][j] = x * sw0;
+      if (GATED) st.s[kSides - 1][j] = x * sw1;
     }
+  }
+  // A step's products.  Each fragment's registers are filled with the next
+  // step's fragment as soon as their last MFMA has been issued.
+  static __device__ __forceinline__ void multiply(State& st, const uint8_t* Al, const uint8_t* Ah, const uint8_t* Bl,
+                                                  const uint8_t* Bh, v4f (*acc)[FB]) {
+    Operand ao, b[FB];
 #pragma unroll
-    for (int j = 0; j < FB; ++j) b[j] = operand(bf[j]);
-    v4f p[kLag + 1];
+    for (int j = 0; j < FB; ++j) b[j] = operand(st.b[j]);
 #pragma unroll
-    for (int q = 0; q < FA * FB + kLag; ++q) {
-      if (q < FA * FB) {
-        const int i = q / FB, j = q % FB;
-        if (j == 0) {
-          if (i + 2 < FA) a[(i + 2) % 3] = fragment(As, a_row + 16 * (i + 2), g);
-          ao = operand(a[i % 3]);
-        }
-        p[q % (kLag + 1)] = product(ao, b[j]);
-        // load l goes after pair l * pairs / loads
+    for (int q = 0; q < FA * FB; ++q) {
+      const int i = q / FB, j = q % FB;
+      if (j == 0) ao = operand(st.a[i]);
+      const int o = (q + FA * FB - kLag) % (FA * FB), oi = o / FB, oj = o % FB;
+      const v4f done = st.p[o % (kLag + 1)];
+      st.p[q % (kLag + 1)] = product(ao, b[j]);
+      if (j == FB - 1) st.a[i] = fragment(Al, Ah, i);
+      if (i == FA - 1) st.b[j] = fragment(Bl, Bh, j);
+      const int side = GATED && oi >= FA / 2 ? 1 : 0;
+      const float f = q >= kLag ? st.s[side][oj] : st.s_last[side][oj];
 #pragma unroll
-        for (int l = 0; l < kLoads; ++l)
-          if (l * (FA * FB) / 2 / kLoads == q) load(l);
-      }
-      if (q >= kLag) {
-        const int i = (q - kLag) / FB, j = (q - kLag) % FB;
-        const float f = s[GATED && i >= FA / 2][j];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(f, p[(q - kLag) % (kLag + 1)][e], acc[i][j][e]);
-      }
+      for (int e = 0; e < 4; ++e) acc[oi][oj][e] = __builtin_fmaf(f, done[e], acc[oi][oj][e]);
       __builtin_amdgcn_sched_barrier(0);  // the scheduler keeps this order
     }
+#pragma unroll
+    for (int k = 0; k < kSides; ++k)
+#pragma unroll
+      for (int j = 0; j < FB; ++j) st.s_last[k][j] = st.s[k][j];
     // the folds stay in this step (the compiler would sink them past the next branch)
 #pragma unroll
     for (int i = 0; i < FA; ++i)
 #pragma unroll
       for (int j = 0; j < FB; ++j) asm volatile("" : "+v"(acc[i][j]));
   }
-
-  // One step: a later step's tiles and a later run's scales (k_s: their byte
-  // offset in a row, or negative) on their way into other buffers, and this
-  // step's products.  Every LDS access of the main loop is in here, behind
-  // pointers that do not overlap (__restrict__), and the loop's first rounds
-  // only load: the compiler then sees that no read touches what a direct load
-  // in flight writes, and adds no wait of its own.
-  static __device__ __forceinline__ void step(bool products, const Source& src, int k_load, int k_s,
-                                              const uint8_t* __restrict__ As, const uint8_t* __restrict__ Bs,
-                                              const float* __restrict__ sx, uint8_t* __restrict__ An,
-                                              uint8_t* __restrict__ Bn, float* __restrict__ sn, float sw0, float sw1,
-                                              v4f (*acc)[FB], int wave, int wn, int wt, int lane) {
-    auto load = [&](int j) { load_piece(j, src, An, Bn, k_load, wave); };
-    if (k_s >= 0) __builtin_amdgcn_raw_ptr_buffer_load_lds(src.xs, (lds_void*)sn, 16, src.vs + k_s, 0, 0, 0);
-    if (products) {
-      multiply(As, Bs, sx, sw0, sw1, acc, wn, wt, lane, load);
-    } else {
+  // The results that the last step has left.
+  static __device__ __forceinline__ void finish(State& st, v4f (*acc)[FB]) {
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) load(j);
+    for (int o = FA * FB - kLag; o < FA * FB; ++o) {
+      const int oi = o / FB, oj = o % FB, side = GATED && oi >= FA / 2 ? 1 : 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        acc[oi][oj][e] = __builtin_fmaf(st.s_last[side][oj], st.p[o % (kLag + 1)][e], acc[oi][oj][e]);
     }
   }
 };
 
-template <int FA, int FB, int WN, int WT, int MODE, int STAGES>
-__global__ __launch_bounds__(64 * WN * WT) void k_dense_fp8(const DenseArgs a) {
-  using D = Tile<FA, FB, WN, WT, MODE, STAGES>;
+template <int FA, int FB, int WN, int WT, int MODE, int STAGES, int NP>
+__global__ __launch_bounds__(64 * (WN * WT + NP)) void k_dense_fp8(const DenseArgs a) {
+  using D = Tile<FA, FB, WN, WT, MODE, STAGES, NP>;
   constexpr int TN = D::TN, TT = D::TT;
   constexpr bool GATED = D::GATED;
   __shared__ __align__(16) uint8_t As[STAGES * TN * kStep], Bs[STAGES * TT * kStep];
@@ -284,80 +285,105 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_fp8(const DenseArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave % WN, wt = wave / WN;
 
-  typename D::Source src;
-  src.w = make_rsrc(a.w + (int64_t)n0 * K, (uint32_t)n_live * K);
-  src.up = GATED ? make_rsrc(a.w + ((int64_t)a.N + n0) * K, (uint32_t)n_live * K) : src.w;
-  src.x = make_rsrc(a.x + t0 * K, (uint32_t)t_live * K);
-  src.xs = make_rsrc(a.xs + t0 * nb, (uint32_t)t_live * nb * 4);
-  int cw[D::kLoadsA], cx[D::kLoadsB];  // the pieces' places within the step
+  if (wave >= D::kWaves) {
+    // ---- loads ----
+    const int p = wave - D::kWaves;
+    typename D::Source src;
+    src.w = make_rsrc(a.w + (int64_t)n0 * K, (uint32_t)n_live * K);
+    src.up = GATED ? make_rsrc(a.w + ((int64_t)a.N + n0) * K, (uint32_t)n_live * K) : src.w;
+    src.x = make_rsrc(a.x + t0 * K, (uint32_t)t_live * K);
+    src.xs = make_rsrc(a.xs + t0 * nb, (uint32_t)t_live * nb * 4);
+    int cw[D::kLoadsA], cx[D::kLoadsB];  // the pieces' places within the step
 #pragma unroll
-  for (int j = 0; j < D::kLoadsA; ++j) {
-    const int r = 8 * (wave * D::kLoadsA + j) + (lane >> 3);
-    const int row = GATED ? D::gated_col(r) : r;
-    cw[j] = ((lane & 7) ^ swz(r)) << 4;
-    src.vw[j] = row < n_live ? row * K + cw[j] : kOutOfRange;
-  }
-#pragma unroll
-  for (int j = 0; j < D::kLoadsB; ++j) {
-    const int r = 8 * (wave * D::kLoadsB + j) + (lane >> 3);
-    cx[j] = ((lane & 7) ^ swz(r)) << 4;
-    src.vx[j] = r < t_live ? r * K + cx[j] : kOutOfRange;
-  }
-  // the last step of a ragged K: chunks past the row's end read as zeros; past
-  // the last step nothing is read (the zeros go to buffers no step uses)
-  const int tail = K % kStep ? K % kStep : kStep;
-  auto cut = [&](int step) {
-    const int end = step >= nb ? 0 : step == nb - 1 ? tail : kStep;
-    if (end < kStep) {
-#pragma unroll
-      for (int j = 0; j < D::kLoadsA; ++j)
-        if (cw[j] >= end) src.vw[j] = kOutOfRange;
-#pragma unroll
-      for (int j = 0; j < D::kLoadsB; ++j)
-        if (cx[j] >= end) src.vx[j] = kOutOfRange;
+    for (int j = 0; j < D::kLoadsA; ++j) {
+      const int r = 8 * (p * D::kLoadsA + j) + (lane >> 3);
+      const int row = GATED ? D::gated_col(r) : r;
+      cw[j] = ((lane & 7) ^ swz(r)) << 4;
+      src.vw[j] = row < n_live ? row * K + cw[j] : kOutOfRange;
     }
-  };
-
-  // Activation scales: a run of kScaleSteps steps at a time, one direct load
-  // for 64 tokens (a lane takes its token's 16 bytes; those past the row's end
-  // belong to no step).  Weight scales: one for the wave's rows and step
-  // (gated: one of the gate rows, one of the up rows), a step ahead in scalar
-  // registers.  (Scales that pass through vector registers make the compiler
-  // wait for every load in flight.)
-  src.vs = (wave * 64 + lane) * nb * 4;
+#pragma unroll
+    for (int j = 0; j < D::kLoadsB; ++j) {
+      const int r = 8 * (p * D::kLoadsB + j) + (lane >> 3);
+      cx[j] = ((lane & 7) ^ swz(r)) << 4;
+      src.vx[j] = r < t_live ? r * K + cx[j] : kOutOfRange;
+    }
+    // the last step of a ragged K: chunks past the row's end read as zeros; past
+    // the last step nothing is read (the zeros go to buffers no step uses)
+    const int tail = K % kStep ? K % kStep : kStep;
+    auto cut = [&](int step) {
+      const int end = step >= nb ? 0 : step == nb - 1 ? tail : kStep;
+      if (end < kStep) {
+#pragma unroll
+        for (int j = 0; j < D::kLoadsA; ++j)
+          if (cw[j] >= end) src.vw[j] = kOutOfRange;
+#pragma unroll
+        for (int j = 0; j < D::kLoadsB; ++j)
+          if (cx[j] >= end) src.vx[j] = kOutOfRange;
+      }
+    };
+    auto load_step = [&](int step, int buf) {
+      cut(step);
+#pragma unroll
+      for (int j = 0; j < D::kLoads; ++j)
+        D::load_piece(j, src, As + buf * TN * kStep, Bs + buf * TT * kStep, step * kStep, p);
+    };
+    // a run's scales: one load for 64 tokens, a lane takes its token's 16 bytes
+    auto load_scales = [&](int run) {
+#pragma unroll
+      for (int q = 0; q < TT / 64; ++q)
+        if (q % NP == p)
+          D::load_16(src.xs, sxs + ((run & 1) * TT + q * 64) * kScaleSteps, ((q * 64 + lane) * nb + run * kScaleSteps) * 4);
+    };
+    // Fragments are read a step ahead: at barrier s step s + 1 has landed and
+    // the buffers of step s are free.
+    load_scales(0);
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) load_step(s, s);
+    loads_done_barrier<(STAGES - 1) * D::kLoads>();
+    int next = 0;
+#pragma unroll 1
+    for (int s = 0; s < nb; ++s) {
+      loads_done_barrier<(STAGES - 2) * D::kLoads>();
+      if ((s & (kScaleSteps - 1)) == 0 && s + kScaleSteps < nb) load_scales(s / kScaleSteps + 1);
+      load_step(s + STAGES, next);
+      next = next + 1 == STAGES ? 0 : next + 1;
+    }
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no load may still write LDS when the workgroup ends
+    if (GATED) lds_barrier();
+    return;
+  }
+  // ---- products ----
+  // weight scales: one for the wave's rows and step (gated: one of the gate
+  // rows, one of the up rows), a step ahead in scalar registers
   const int nbn = (a.N + kFp8Block - 1) / kFp8Block;
   const int blk = GATED ? n0 / kFp8Block : min((n0 + wn * 16 * FA) / kFp8Block, nbn - 1);
   typedef const __attribute__((address_space(4))) float* const_floats;
   const const_floats ws0 = (const_floats)(a.ws + (int64_t)blk * nb);
   const const_floats ws1 = (const_floats)(a.ws + (int64_t)(blk + (GATED ? nbn : 0)) * nb);
-
-  // Round s loads step s + kAhead and multiplies step s; the first rounds only
-  // load.  A run's scales are loaded in the first round of the run before it
-  // (run 0's in the first round of all).
-  constexpr int kAhead = STAGES - 1;
   v4f acc[FA][FB] = {};
-  int cur = 0, next = 0;  // buffers of the step multiplied, and of the step loaded
+  typename D::State st = {};
+  const int a_off = D::lane_offset(wn * 16 * FA + (lane & 15), lane >> 4);
+  const int b_off = D::lane_offset(wt * 16 * FB + (lane & 15), lane >> 4);
+  const float* sx = sxs + (wt * 16 * FB + (lane & 15)) * kScaleSteps;
+  loads_done_barrier<63>();  // step 0 has landed
+#pragma unroll
+  for (int i = 0; i < FA; ++i) st.a[i] = D::fragment(As + a_off, As + (a_off ^ 64), i);
+#pragma unroll
+  for (int j = 0; j < FB; ++j) st.b[j] = D::fragment(Bs + b_off, Bs + (b_off ^ 64), j);
+  int cur = 1;
   float sw0 = ws0[0], sw1 = ws1[0];
 #pragma unroll 1
-  for (int s = -kAhead; s < nb; ++s) {
-    // this step's tiles have landed (later ones may be on their way), and
-    // every wave has left the step whose buffers are loaded now
-    loads_done_barrier<(kAhead - 1) * D::kLoads>();
-    cut(s + kAhead);
-    const int run = s >> kScaleShift, at = s & (kScaleSteps - 1), later = s < 0 ? 0 : run + 1;
-    const bool scales = (at == 0 || s == -kAhead) && wave < TT / 64 && later * kScaleSteps < nb;
-    const int ahead = max(0, min(s + 1, nb - 1));
-    const float sw0_next = ws0[ahead], sw1_next = ws1[ahead];
-    D::step(s >= 0, src, (s + kAhead) * kStep, scales ? later * kScaleSteps * 4 : -1, As + cur * TN * kStep,
-            Bs + cur * TT * kStep, sxs + (run & 1) * TT * kScaleSteps + at, As + next * TN * kStep,
-            Bs + next * TT * kStep, sxs + ((later & 1) * TT + wave * 64) * kScaleSteps, sw0, sw1, acc, wave, wn, wt,
-            lane);
-    sw0 = sw0_next;
-    sw1 = sw1_next;
-    if (s >= 0) cur = cur + 1 == STAGES ? 0 : cur + 1;
-    next = next + 1 == STAGES ? 0 : next + 1;
+  for (int s = 0; s < nb; ++s) {
+    loads_done_barrier<63>();
+    D::scales(st, sx + ((s >> kScaleShift) & 1) * TT * kScaleSteps + (s & (kScaleSteps - 1)), sw0, sw1);
+    const int ahead = min(s + 1, nb - 1);
+    sw0 = ws0[ahead];
+    sw1 = ws1[ahead];
+    const int al = cur * TN * kStep + a_off, bl = cur * TT * kStep + b_off;
+    D::multiply(st, As + al, As + (al ^ 64), Bs + bl, Bs + (bl ^ 64), acc);
+    cur = cur + 1 == STAGES ? 0 : cur + 1;
   }
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no load may still write LDS when the workgroup ends
+  D::finish(st, acc);
 
   const int r = lane & 15, g = lane >> 4;
   if constexpr (!GATED) {
@@ -503,13 +529,13 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_fp8(const DenseArgs a) {
   }
 }
 
-template <int FA, int FB, int WN, int WT, int MODE, int STAGES>
+template <int FA, int FB, int WN, int WT, int MODE, int STAGES, int NP>
 hipError_t run(DenseArgs a, hipStream_t st) {
-  using D = Tile<FA, FB, WN, WT, MODE, STAGES>;
+  using D = Tile<FA, FB, WN, WT, MODE, STAGES, NP>;
   const int tn = MODE == kGated ? D::TN / 2 : D::TN;
   a.n_nt = (a.N + tn - 1) / tn;
   a.n_tt = (int)((a.T + D::TT - 1) / D::TT);
-  hipLaunchKernelGGL((k_dense_fp8<FA, FB, WN, WT, MODE, STAGES>), dim3((unsigned)(a.n_nt * a.n_tt)), dim3(D::kThreads),
+  hipLaunchKernelGGL((k_dense_fp8<FA, FB, WN, WT, MODE, STAGES, NP>), dim3((unsigned)(a.n_nt * a.n_tt)), dim3(D::kThreads),
                      0, st, a);
   return hipGetLastError();
 }
@@ -525,14 +551,12 @@ struct Variant {
   int per_cu;        // tiles a CU holds (LDS)
   float fixed, step[4];
 };
-constexpr Variant kFastTiles[] = {{256, 256, 1, 9.f, {1.68f}},
-                                  {128, 128, 2, 6.f, {0.84f, 1.02f}},
-                                  {128, 64, 3, 5.f, {0.62f, 0.74f, 0.93f}},
-                                  {64, 64, 4, 4.f, {0.45f, 0.60f, 0.71f, 0.79f}}};
-constexpr Variant kExactTiles[] = {{128, 128, 2, 7.f, {1.04f, 1.73f}},
-                                   {128, 64, 3, 6.f, {0.72f, 1.09f, 1.50f}},
-                                   {64, 64, 4, 5.f, {0.55f, 0.69f, 0.95f, 1.22f}}};
-constexpr Variant kGatedTiles[] = {{128, 256, 1, 9.f, {1.62f}}, {128, 128, 1, 9.f, {0.95f}}, {128, 64, 1, 6.f, {0.65f}}};
+constexpr Variant kFastTiles[] = {{256, 128, 1, 6.f, {0.86f}},
+                                  {128, 128, 1, 5.f, {0.46f}},
+                                  {128, 64, 2, 4.f, {0.32f, 0.65f}},
+                                  {64, 64, 2, 3.f, {0.20f, 0.39f}}};
+constexpr Variant kExactTiles[] = {{128, 128, 1, 6.f, {0.92f}}, {64, 64, 2, 4.f, {0.35f, 0.57f}}};
+constexpr Variant kGatedTiles[] = {{128, 128, 1, 7.f, {0.86f}}, {128, 64, 1, 5.f, {0.50f}}};
 
 template <int COUNT>
 int pick(const Variant (&v)[COUNT], int64_t T, int N, int nb, int num_cus) {
@@ -557,28 +581,22 @@ hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w,
                             int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus, hipStream_t st) {
   const DenseArgs a{x, xs, w, ws, y_f32, y_bf16, y_q8, nullptr, nullptr, T, N, K, (K + kStep - 1) / kStep, 0, 0};
   if (y_f32) {  // exact products (see the head of the file)
-    switch (pick(kExactTiles, T, N, a.nb, num_cus)) {
-      case 0: return run<4, 4, 2, 2, kExact, 2>(a, st);
-      case 1: return run<4, 2, 2, 2, kExact, 2>(a, st);
-      default: return run<2, 2, 2, 2, kExact, 2>(a, st);
-    }
+    if (pick(kExactTiles, T, N, a.nb, num_cus) == 0) return run<4, 4, 2, 2, kExact, 3, 2>(a, st);
+    return run<2, 2, 2, 2, kExact, 4, 4>(a, st);
   }
   switch (pick(kFastTiles, T, N, a.nb, num_cus)) {
-    case 0: return run<8, 4, 2, 4, kFast, 2>(a, st);
-    case 1: return run<4, 4, 2, 2, kFast, 2>(a, st);
-    case 2: return run<4, 2, 2, 2, kFast, 2>(a, st);
-    default: return run<2, 2, 2, 2, kFast, 2>(a, st);
+    case 0: return run<4, 4, 4, 2, kFast, 3, 4>(a, st);
+    case 1: return run<4, 4, 2, 2, kFast, 3, 4>(a, st);
+    case 2: return run<4, 2, 2, 2, kFast, 3, 2>(a, st);
+    default: return run<2, 2, 2, 2, kFast, 4, 4>(a, st);
   }
 }
 
 hipError_t launch_gateup_fp8(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int64_t T, int F,
                              int C, uint8_t* h, float* hs, int num_cus, hipStream_t st) {
   const DenseArgs a{x, xs, gu, gus, nullptr, nullptr, nullptr, h, hs, T, F, C, (C + kStep - 1) / kStep, 0, 0};
-  switch (pick(kGatedTiles, T, F, a.nb, num_cus)) {
-    case 0: return run<8, 4, 2, 4, kGated, 2>(a, st);
-    case 1: return run<4, 4, 4, 2, kGated, 3>(a, st);
-    default: return run<8, 2, 2, 2, kGated, 3>(a, st);
-  }
+  if (pick(kGatedTiles, T, F, a.nb, num_cus) == 0) return run<4, 4, 4, 2, kGated, 3, 4>(a, st);
+  return run<8, 2, 2, 2, kGated, 3, 4>(a, st);
 }
 
 }  // namespace latmoe
