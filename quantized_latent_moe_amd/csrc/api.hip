@@ -1,4 +1,5 @@
 // C ABI of the expert stage: argument checks, workspace layout, launches.
+#include <algorithm>
 #include <mutex>
 #include <string.h>
 
@@ -217,7 +218,8 @@ bool fp8_dense_ok(int64_t T, int32_t N, int32_t K) {
 }
 hipError_t dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int64_t T, int N, int K,
                      float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus, hipStream_t st) {
-  if (T <= kFp8SmallT) return launch_dense_fp8_small(x, xs, w, ws, (int)T, N, K, y_f32, y_bf16, y_q8, st);
+  if (T <= (y_f32 ? kFp8SmallExactT : kFp8SmallT))
+    return launch_dense_fp8_small(x, xs, w, ws, (int)T, N, K, y_f32, y_bf16, y_q8, st);
   return launch_dense_fp8(x, xs, w, ws, T, N, K, y_f32, y_bf16, y_q8, num_cus, st);
 }
 
@@ -226,7 +228,8 @@ bool ffn_fp8_ok(int64_t T, int32_t C, int32_t F) {
   return fp8_dense_ok(T, F, C) && fp8_dense_ok(T, C, F) && fp8_cols_ok(F) && (int64_t)2 * F * C < (int64_t)1 << 31;
 }
 // Workspace of the gated block: H's codes and scales, and for few tokens the
-// fp32 H that they are rounded from.
+// fp32 H that they are rounded from.  The size does not fall as T grows: a
+// workspace for a largest batch holds every smaller one.
 struct FfnLayout {
   size_t codes, scales, h32, total;
 };
@@ -235,7 +238,8 @@ FfnLayout ffn_layout(int64_t T, int32_t F) {
   size_t o = 0;
   L.codes = o;  o = align_up(o + (size_t)T * F);
   L.scales = o; o = align_up(o + sizeof(float) * (size_t)(T * fp8_blocks(F)));
-  L.h32 = o;    o = align_up(o + (T <= kFp8SmallT ? sizeof(float) * (size_t)T * F : 0));
+  const int64_t h32 = std::max(std::min<int64_t>(T, kFp8SmallT) * F, std::min<int64_t>(T * F, kFp8H32));
+  L.h32 = o;    o = align_up(o + sizeof(float) * (size_t)h32);
   L.total = o > kAlign ? o : kAlign;
   return L;
 }
@@ -422,17 +426,22 @@ int lat_moe_ffn_fp8(const void* x_fp8, const float* x_scales, const void* gateup
   const uint8_t* gu = static_cast<const uint8_t*>(gateup_fp8);
   uint8_t* h = h_fp8 ? static_cast<uint8_t*>(h_fp8) : reinterpret_cast<uint8_t*>(ws + L.codes);
   float* hs = h_fp8 ? h_scales : reinterpret_cast<float*>(ws + L.scales);
+  float* h32 = reinterpret_cast<float*>(ws + L.h32);
   if (T <= kFp8SmallT) {
-    float* h32 = reinterpret_cast<float*>(ws + L.h32);
     if (launch_gateup_fp8_small(x, x_scales, gu, gateup_scales, (int)T, F, C, h32, st) != hipSuccess)
       return LAT_MOE_ELAUNCH;
-    if (T <= kFp8RoundT && !h_fp8)  // H's codes are not asked for: the down projection rounds H as it reads it
+    // where H's codes are not asked for, the down projection may round H as it
+    // reads it: a launch less, but a second block of K for a wave would wait for
+    // the first (C = 4096, F = 2048, us for 1, 4, 8 tokens: 9.3, 10.2, 11.3, and
+    // 10.1, 10.8, 11.7 with a launch for the rounding; C = 1024, F = 4096: 9.9,
+    // 11.2, 12.6 and 10.1, 10.8, 11.5)
+    if (T <= kFp8RoundT && F <= kFp8RoundK && !h_fp8)
       return launch_dense_fp8_round(h32, static_cast<const uint8_t*>(down_fp8), down_scales, (int)T, C, F, y_f32,
                                     static_cast<uint16_t*>(y_bf16), st) == hipSuccess
                  ? LAT_MOE_OK
                  : LAT_MOE_ELAUNCH;
     if (launch_quantize_fp8(h32, LAT_MOE_F32, T, F, h, hs, st) != hipSuccess) return LAT_MOE_ELAUNCH;
-  } else if (launch_gateup_fp8(x, x_scales, gu, gateup_scales, T, F, C, h, hs, num_cus, st) != hipSuccess) {
+  } else if (launch_gateup_fp8(x, x_scales, gu, gateup_scales, T, F, C, h32, h, hs, num_cus, st) != hipSuccess) {
     return LAT_MOE_ELAUNCH;
   }
   if (dense_fp8(h, hs, static_cast<const uint8_t*>(down_fp8), down_scales, T, C, F, y_f32,

@@ -126,4 +126,6 @@ __device__ __forceinline__ uint2 e4m3_block(const float* v, float& scale) {
                pack_e4m3(v[4] * id, v[5] * id, v[6] * id, v[7] * id)};
 }
 
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
+
 }  // namespace latmoe

@@ -112,12 +112,13 @@ __device__ __forceinline__ void tile_of(const DenseArgs& a, int& nt, int& tt) {
 }
 
 // What a tile kernel computes: the projection with e4m3 products, the
-// projection with bf16 products, or the gated pair of projections.
-enum Mode : int { kFast = 0, kExact = 1, kGated = 2 };
+// projection with bf16 products, or the gated pair of projections with H
+// rounded to e4m3 (a tile then holds 128 columns of H, one scale's) or in fp32.
+enum Mode : int { kFast = 0, kExact = 1, kGated = 2, kGatedRaw = 3 };
 
 template <int FA, int FB, int WN, int WT, int MODE, int STAGES, int NP>
 struct Tile {
-  static constexpr bool GATED = MODE == kGated;
+  static constexpr bool GATED = MODE == kGated || MODE == kGatedRaw;
   static constexpr int kWaves = WN * WT;                // that multiply; NP more load
   static constexpr int kThreads = 64 * (kWaves + NP);
   static constexpr int TN = 16 * FA * WN, TT = 16 * FB * WT;
@@ -126,7 +127,7 @@ struct Tile {
   static_assert(TN % (8 * NP) == 0 && TT % (8 * NP) == 0, "whole loads");
   static_assert(TT % 64 == 0, "a load takes 64 tokens' scales");
   static_assert(STAGES >= 2, "at least a step ahead");
-  static_assert(!GATED || TN == 256, "a gated tile holds one e4m3 block of H");
+  static_assert(MODE != kGated || TN == 256, "a gated tile holds one e4m3 block of H");
 
   // H column (within the tile) of LDS row r of the weight tile, gated tiles:
   // each wave's 16 FA rows are FA/2 gate fragments and the same columns' up
@@ -272,7 +273,7 @@ __global__ __launch_bounds__(64 * (WN * WT + NP)) void k_dense_fp8(const DenseAr
   constexpr bool GATED = D::GATED;
   __shared__ __align__(16) uint8_t As[STAGES * TN * kStep], Bs[STAGES * TT * kStep];
   __shared__ __align__(16) float sxs[2 * TT * kScaleSteps];  // two runs of [token][step]
-  __shared__ float part[GATED ? WN : 1][GATED ? TT : 1];  // largest |H| of a token in a wave's columns
+  __shared__ float part[MODE == kGated ? WN : 1][MODE == kGated ? TT : 1];  // largest |H| of a token in a wave's columns
 
   int nt, tt;
   tile_of(a, nt, tt);
@@ -349,7 +350,7 @@ __global__ __launch_bounds__(64 * (WN * WT + NP)) void k_dense_fp8(const DenseAr
       next = next + 1 == STAGES ? 0 : next + 1;
     }
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no load may still write LDS when the workgroup ends
-    if (GATED) lds_barrier();
+    if (MODE == kGated) lds_barrier();
     return;
   }
   // ---- products ----
@@ -386,7 +387,18 @@ __global__ __launch_bounds__(64 * (WN * WT + NP)) void k_dense_fp8(const DenseAr
   D::finish(st, acc);
 
   const int r = lane & 15, g = lane >> 4;
-  if constexpr (!GATED) {
+  if constexpr (MODE == kGatedRaw) {
+#pragma unroll
+    for (int j = 0; j < FB; ++j)
+#pragma unroll
+      for (int i = 0; i < FA / 2; ++i) {
+        const int tl = wt * 16 * FB + 16 * j + r, n = wn * 8 * FA + 16 * i + 4 * g;
+        v4f h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = silu(acc[i][j][e]) * acc[i + FA / 2][j][e];
+        if (tl < t_live && n < n_live) *reinterpret_cast<v4f*>(a.y_f32 + (t0 + tl) * a.N + n0 + n) = h;
+      }
+  } else if constexpr (!GATED) {
     const bool vec4 = a.N % 4 == 0, vec8 = a.N % 8 == 0;
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
@@ -485,8 +497,7 @@ __global__ __launch_bounds__(64 * (WN * WT + NP)) void k_dense_fp8(const DenseAr
       for (int i = 0; i < FA / 2; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float gv = acc[i][j][e];
-          const float h = gv / (1.0f + __expf(-gv)) * acc[i + FA / 2][j][e];
+          const float h = silu(acc[i][j][e]) * acc[i + FA / 2][j][e];
           acc[i][j][e] = h;
           amax = fmaxf(amax, fabsf(h));
         }
@@ -532,7 +543,7 @@ __global__ __launch_bounds__(64 * (WN * WT + NP)) void k_dense_fp8(const DenseAr
 template <int FA, int FB, int WN, int WT, int MODE, int STAGES, int NP>
 hipError_t run(DenseArgs a, hipStream_t st) {
   using D = Tile<FA, FB, WN, WT, MODE, STAGES, NP>;
-  const int tn = MODE == kGated ? D::TN / 2 : D::TN;
+  const int tn = D::GATED ? D::TN / 2 : D::TN;
   a.n_nt = (a.N + tn - 1) / tn;
   a.n_tt = (int)((a.T + D::TT - 1) / D::TT);
   hipLaunchKernelGGL((k_dense_fp8<FA, FB, WN, WT, MODE, STAGES, NP>), dim3((unsigned)(a.n_nt * a.n_tt)), dim3(D::kThreads),
@@ -556,13 +567,19 @@ constexpr Variant kFastTiles[] = {{256, 128, 1, 6.f, {0.86f}},
                                   {128, 64, 2, 4.f, {0.32f, 0.65f}},
                                   {64, 64, 2, 3.f, {0.20f, 0.39f}}};
 constexpr Variant kExactTiles[] = {{128, 128, 1, 6.f, {0.92f}}, {64, 64, 2, 4.f, {0.35f, 0.57f}}};
-constexpr Variant kGatedTiles[] = {{128, 128, 1, 7.f, {0.86f}}, {128, 64, 1, 5.f, {0.50f}}};
+constexpr Variant kGatedTiles[] = {{128, 128, 1, 7.f, {0.86f}}, {128, 64, 1, 5.f, {0.50f}},
+                                   // with the rounding in a launch of its own
+                                   {64, 64, 2, 7.f, {0.32f, 0.65f}}, {32, 64, 2, 6.f, {0.20f, 0.39f}}};
+// Variants that round H themselves.  128 columns of H are one scale's, so these
+// fill the chip only where T F is large: 65 tokens of C = 4096, F = 2048 (16
+// tiles of 128 x 64) took 24.0 us for the whole block, and take 16.9 us with
+// tiles of 32 columns, fp32 H and a launch that rounds it.
+constexpr int kGatedRounded = 2;
 
-template <int COUNT>
-int pick(const Variant (&v)[COUNT], int64_t T, int N, int nb, int num_cus) {
+int pick(const Variant* v, int count, int64_t T, int N, int nb, int num_cus) {
   int best = 0;
   float least = 0.f;
-  for (int i = 0; i < COUNT; ++i) {
+  for (int i = 0; i < count; ++i) {
     const int64_t tiles = ((T + v[i].tokens - 1) / v[i].tokens) * ((N + v[i].cols - 1) / v[i].cols);
     const int64_t slots = (int64_t)num_cus * v[i].per_cu, passes = tiles / slots, rest = tiles % slots;
     float t = (float)passes * (v[i].step[v[i].per_cu - 1] * (float)nb + v[i].fixed);
@@ -581,10 +598,10 @@ hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w,
                             int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus, hipStream_t st) {
   const DenseArgs a{x, xs, w, ws, y_f32, y_bf16, y_q8, nullptr, nullptr, T, N, K, (K + kStep - 1) / kStep, 0, 0};
   if (y_f32) {  // exact products (see the head of the file)
-    if (pick(kExactTiles, T, N, a.nb, num_cus) == 0) return run<4, 4, 2, 2, kExact, 3, 2>(a, st);
+    if (pick(kExactTiles, 2, T, N, a.nb, num_cus) == 0) return run<4, 4, 2, 2, kExact, 3, 2>(a, st);
     return run<2, 2, 2, 2, kExact, 4, 4>(a, st);
   }
-  switch (pick(kFastTiles, T, N, a.nb, num_cus)) {
+  switch (pick(kFastTiles, 4, T, N, a.nb, num_cus)) {
     case 0: return run<4, 4, 4, 2, kFast, 3, 4>(a, st);
     case 1: return run<4, 4, 2, 2, kFast, 3, 4>(a, st);
     case 2: return run<4, 2, 2, 2, kFast, 3, 2>(a, st);
@@ -593,10 +610,14 @@ hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w,
 }
 
 hipError_t launch_gateup_fp8(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int64_t T, int F,
-                             int C, uint8_t* h, float* hs, int num_cus, hipStream_t st) {
-  const DenseArgs a{x, xs, gu, gus, nullptr, nullptr, nullptr, h, hs, T, F, C, (C + kStep - 1) / kStep, 0, 0};
-  if (pick(kGatedTiles, T, F, a.nb, num_cus) == 0) return run<4, 4, 4, 2, kGated, 3, 4>(a, st);
-  return run<8, 2, 2, 2, kGated, 3, 4>(a, st);
+                             int C, float* h32, uint8_t* h, float* hs, int num_cus, hipStream_t st) {
+  const DenseArgs a{x, xs, gu, gus, h32, nullptr, nullptr, h, hs, T, F, C, (C + kStep - 1) / kStep, 0, 0};
+  const int variant = pick(kGatedTiles, T * F <= kFp8H32 ? 4 : kGatedRounded, T, F, a.nb, num_cus);
+  if (variant == 0) return run<4, 4, 4, 2, kGated, 3, 4>(a, st);
+  if (variant == 1) return run<8, 2, 2, 2, kGated, 3, 4>(a, st);
+  const hipError_t e =
+      variant == 2 ? run<4, 2, 2, 2, kGatedRaw, 3, 2>(a, st) : run<2, 2, 2, 2, kGatedRaw, 4, 4>(a, st);
+  return e == hipSuccess ? launch_quantize_fp8(h32, LAT_MOE_F32, T, F, h, hs, st) : e;
 }
 
 }  // namespace latmoe

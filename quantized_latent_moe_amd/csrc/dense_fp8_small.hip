@@ -1,20 +1,30 @@
-// Products of e4m3 rows with e4m3 weights for at most kFp8SmallT tokens
-// (decode): the formulas of the tile kernel, arranged to stream the weights.
+// Products of e4m3 rows with e4m3 weights for few tokens (decode): the formulas
+// of the tile kernel, arranged to stream the weights.
 //
 // Each weight is used for a few tokens only, so the time is that of reading
 // the weights once, and the products are exact: codes are widened to bf16 for
-// the bf16 MFMA, whatever the output type.  A workgroup takes 16 FR weight rows whole: its 8 waves
-// deal the blocks of K = 128 among themselves, load fragments straight from
-// memory into registers (no LDS on the way in; a lane's two 16-byte pieces lie
-// 64 bytes apart, so each load covers 64 contiguous bytes of a row), several
-// blocks ahead, and add their partial sums in LDS at the end, in wave order:
-// the result does not depend on timing.
+// the bf16 MFMA, whatever the output type.  A workgroup takes 16 FR weight rows
+// whole: its waves deal the blocks of K = 128 among themselves, load fragments
+// straight from memory into registers (no LDS on the way in; a lane's two
+// 16-byte pieces lie 64 bytes apart, so each load covers 64 contiguous bytes of
+// a row), and add their partial sums in LDS at the end, in wave order: the
+// result does not depend on timing.
+//
+// What bounds it: launch, the latency of one or two reads in a row, and the
+// adding of partial sums; then the weights' rate.  In a captured graph a
+// product of 4 tokens takes 3.0 us for 4096 x 1024 weights, 5.3 us for
+// 4096 x 4096 (16 MB, 3.2 TB/s) and 5.1 us for 8192 x 2048.
+//
+// Against the tiles (us, 16 | 17 .. 32 tokens here and in tiles):
+//   4096 x 4096:  7.0 | 7.8 .. 9.6, bf16 tiles 8.7, fp32 (exact) tiles 13.4
+//   8192 x 2048:  6.7 | 7.3 .. 9.4, bf16 tiles 6.0, fp32 (exact) tiles 8.4
+// so a call for rounded outputs comes here up to 16 tokens, one for the fp32 y
+// up to 32 (beyond, a fragment of 16 tokens more costs 3 us and more).
 #include "block_fp8.h"
 
 namespace latmoe {
 namespace {
 
-constexpr int kWaves = 8;
 
 struct SmallArgs {
   const uint8_t* x;  // [T][K] e4m3, or null: the rows are h32
@@ -41,15 +51,21 @@ __device__ __forceinline__ void widen16(const uint4* p, v8bf* o) {
 // weight rows are 8 gate rows and the same columns' 8 up rows, so that one
 // fragment holds both and twice as many workgroups share the weights); a
 // projection of fp32 rows that it rounds to e4m3 itself (every workgroup
-// rounds them again, which for 16 tokens costs less than a launch between).
+// rounds them again, which for few tokens costs less than a launch between).
 enum SmallMode : int { kRows = 0, kGatedPair = 1, kRound = 2 };
 
 // Token columns past T and weight rows past N hold zeros or a clamped row;
 // they meet only results that are not stored.
+// Waves of a workgroup, each with TF blocks in flight.  For 16 tokens 16 waves
+// with one block each take 3.0 us for 4096 x 1024 weights and 4.8 us for
+// 8192 x 2048, eight with four each 3.6 and 5.7 us (the wave's own chain of
+// blocks is as long, and few blocks leave it waiting for the last).
+constexpr int small_waves(int tf) { return tf == 1 ? 16 : 8; }
+
 template <int FR, int TF, int MODE>
-__global__ __launch_bounds__(64 * kWaves) void k_dense_fp8_small(const SmallArgs a) {
+__global__ __launch_bounds__(64 * small_waves(TF)) void k_dense_fp8_small(const SmallArgs a) {
   constexpr bool GATED = MODE == kGatedPair;
-  constexpr int U = MODE == kRound || TF > 1 ? 2 : 4;  // blocks in flight per wave
+  constexpr int kWaves = small_waves(TF), U = TF;  // U blocks in flight per wave
   constexpr int NF = GATED ? 8 : 16 * FR;              // output columns
   static_assert(!GATED || FR == 1, "one fragment of gate and up rows");
   static_assert(MODE != kRound || TF == 1, "rounding for 16 tokens");
@@ -177,7 +193,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_fp8_small(const SmallArgs
     float v = total(c, t);
     if constexpr (GATED) {
       const float u = total(8 + c, t);
-      v = v / (1.0f + __expf(-v)) * u;
+      v = silu(v) * u;
     }
     if (live && a.y_f32) a.y_f32[(int64_t)t * a.N + n] = v;
     if (live && a.y_bf16) a.y_bf16[(int64_t)t * a.N + n] = (uint16_t)pack_bf16(v, v);
@@ -209,14 +225,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_fp8_small(const SmallArgs
 template <int FR, int MODE>
 void run(const SmallArgs& a, hipStream_t st) {
   const int nf = MODE == kGatedPair ? 8 : 16 * FR;
-  const dim3 grid((unsigned)((a.N + nf - 1) / nf)), block(64 * kWaves);
-  if constexpr (MODE == kRound) {
-    hipLaunchKernelGGL((k_dense_fp8_small<FR, 1, MODE>), grid, block, 0, st, a);
-  } else {
-    if (a.T <= 16) hipLaunchKernelGGL((k_dense_fp8_small<FR, 1, MODE>), grid, block, 0, st, a);
-    else if (a.T <= 32) hipLaunchKernelGGL((k_dense_fp8_small<FR, 2, MODE>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((k_dense_fp8_small<FR, 4, MODE>), grid, block, 0, st, a);
+  const dim3 grid((unsigned)((a.N + nf - 1) / nf));
+  if constexpr (MODE == kRows) {
+    if (a.T > 16) {
+      hipLaunchKernelGGL((k_dense_fp8_small<FR, 2, MODE>), grid, dim3(64 * small_waves(2)), 0, st, a);
+      return;
+    }
   }
+  hipLaunchKernelGGL((k_dense_fp8_small<FR, 1, MODE>), grid, dim3(64 * small_waves(1)), 0, st, a);
 }
 
 }  // namespace

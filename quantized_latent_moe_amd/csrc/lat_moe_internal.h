@@ -255,19 +255,23 @@ hipError_t launch_rmsnorm(const NormArgs& a, int num_cus, hipStream_t st);
 // e4m3 rows [T][K] x e4m3 weights [N][K] -> y in fp32, bf16 and/or q8_1 (any may be null, not all).
 hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int64_t T, int N,
                             int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus, hipStream_t st);
-// The same for at most kFp8SmallT tokens, by a kernel that streams the weights.
-constexpr int kFp8SmallT = 64;
+// The same for at most kFp8SmallT tokens (kFp8SmallExactT where the fp32 y is
+// asked for), by a kernel that streams the weights.
+constexpr int kFp8SmallT = 16, kFp8SmallExactT = 32;
 hipError_t launch_dense_fp8_small(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int T, int N,
                                   int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, hipStream_t st);
 // fp32 rows h [T][K] of at most kFp8RoundT tokens, rounded to e4m3 rows on the way, x e4m3 weights.
-constexpr int kFp8RoundT = 16;
+constexpr int kFp8RoundT = 8, kFp8RoundK = 2048;
 hipError_t launch_dense_fp8_round(const float* h, const uint8_t* w, const float* ws, int T, int N, int K, float* y_f32,
                                   uint16_t* y_bf16, hipStream_t st);
 // silu(G) * U of at most kFp8SmallT tokens, unrounded: h [T][F] fp32.
 hipError_t launch_gateup_fp8_small(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int T,
                                    int F, int C, float* h, hipStream_t st);
-// Gate and up projections (gu [2F][C]: gate rows, then up rows), silu(G) * U, rounded to e4m3 rows h [T][F].
+// Gate and up projections (gu [2F][C]: gate rows, then up rows), silu(G) * U,
+// rounded to e4m3 rows h [T][F].  Up to kFp8H32 values of H may take the way
+// through h32 [T][F] (not read before it is written).
+constexpr int64_t kFp8H32 = (int64_t)1 << 20;
 hipError_t launch_gateup_fp8(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int64_t T, int F,
-                             int C, uint8_t* h, float* hs, int num_cus, hipStream_t st);
+                             int C, float* h32, uint8_t* h, float* hs, int num_cus, hipStream_t st);
 
 }  // namespace latmoe
