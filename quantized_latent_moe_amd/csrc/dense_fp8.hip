@@ -206,7 +206,11 @@ struct Tile {
 
   // What a multiplying wave carries from step to step: the fragments and
   // scales of the step in hand, and the results that are not folded yet.
-  static constexpr int kLag = 3;  // an MFMA's result is folded three MFMAs later
+  // A product is folded kLag products later.  Where two multiplying waves of a
+  // SIMD cover each other's waits and bf16 operands fill the registers, one is
+  // enough; a wave alone (128 x 128 exact) takes 44 us with 1 and 37 with 3 for
+  // 2048 x 2048 x 4096.
+  static constexpr int kLag = MODE == kExact && kWaves == 8 ? 1 : 3;
   static constexpr int kSides = GATED ? 2 : 1;
   static_assert(FA * FB % (kLag + 1) == 0, "the results' registers come round with the step");
   struct State {
@@ -566,7 +570,8 @@ constexpr Variant kFastTiles[] = {{256, 128, 1, 6.f, {0.86f}},
                                   {128, 128, 1, 5.f, {0.46f}},
                                   {128, 64, 2, 4.f, {0.32f, 0.65f}},
                                   {64, 64, 2, 3.f, {0.20f, 0.39f}}};
-constexpr Variant kExactTiles[] = {{128, 128, 1, 6.f, {0.92f}}, {64, 64, 2, 4.f, {0.35f, 0.57f}}};
+constexpr Variant kExactTiles[] = {
+    {128, 192, 1, 7.f, {1.42f}}, {128, 128, 1, 6.f, {0.92f}}, {64, 64, 2, 4.f, {0.35f, 0.57f}}};
 constexpr Variant kGatedTiles[] = {{128, 128, 1, 7.f, {0.86f}}, {128, 64, 1, 5.f, {0.50f}},
                                    // with the rounding in a launch of its own
                                    {64, 64, 2, 7.f, {0.32f, 0.65f}}, {32, 64, 2, 6.f, {0.20f, 0.39f}}};
@@ -598,8 +603,11 @@ hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w,
                             int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus, hipStream_t st) {
   const DenseArgs a{x, xs, w, ws, y_f32, y_bf16, y_q8, nullptr, nullptr, T, N, K, (K + kStep - 1) / kStep, 0, 0};
   if (y_f32) {  // exact products (see the head of the file)
-    if (pick(kExactTiles, 2, T, N, a.nb, num_cus) == 0) return run<4, 4, 2, 2, kExact, 3, 2>(a, st);
-    return run<2, 2, 2, 2, kExact, 4, 4>(a, st);
+    switch (pick(kExactTiles, 3, T, N, a.nb, num_cus)) {
+      case 0: return run<4, 3, 2, 4, kExact, 3, 4>(a, st);
+      case 1: return run<4, 4, 2, 2, kExact, 3, 2>(a, st);
+      default: return run<2, 2, 2, 2, kExact, 4, 4>(a, st);
+    }
   }
   switch (pick(kFastTiles, 4, T, N, a.nb, num_cus)) {
     case 0: return run<4, 4, 4, 2, kFast, 3, 4>(a, st);

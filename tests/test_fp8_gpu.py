@@ -105,7 +105,8 @@ def test_dense_matches_oracle(T, N, K):
 
 
 # many token and weight tiles: the tile order, and every variant's edges
-@pytest.mark.parametrize("T,N,K", [(2100, 544, 528), (5268, 1024, 256), (4133, 2052, 144), (700, 4096, 128), (9000, 96, 384)])
+@pytest.mark.parametrize("T,N,K", [(2100, 544, 528), (5268, 1024, 256), (4133, 2052, 144), (700, 4096, 128), (9000, 96, 384),
+                                   (1500, 2070, 656), (2100, 2067, 528)])
 def test_dense_of_many_tiles(T, N, K):
     rng = np.random.default_rng(T)
     (x, xs), (w, ws) = _x(rng, T, K), _w(rng, N, K)
