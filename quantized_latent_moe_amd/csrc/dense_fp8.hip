@@ -35,7 +35,12 @@
 //
 // What bounds it: direct loads reach about 100 GB/s a CU, 0.48 us for a step
 // of 256 x 128, and the MFMAs of that step take 0.5 to 0.57 us (the clock
-// falls to 1.8 GHz under them); together, with the LDS reads between, 0.87 us.
+// falls to 1.8 GHz under them); together, with the LDS reads between, 0.86 us.  A
+// small tile's step is a chain (barrier, LDS reads, MFMAs, barrier): 0.20 us
+// for 64 x 64 on one CU, whatever the number of stages.  21000 x 4096 rows by
+// 4096 weights take 347 us (2030 TF; as much through the bf16 MFMA with an fp32
+// y 640 us, 1100 TF).
+#include <algorithm>
 #include <type_traits>
 
 #include "block_fp8.h"
@@ -47,7 +52,8 @@ typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int kXcds = 8;
 constexpr int kStep = kFp8Block;  // K per step: one MFMA, one scale
-constexpr int kScaleShift = 2, kScaleSteps = 1 << kScaleShift;  // steps whose scales are staged together
+constexpr int kScaleSteps = 4;  // a run: steps whose scales are staged together
+constexpr int kRunBuffers = 4;
 
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 
@@ -99,9 +105,9 @@ struct DenseArgs {
 // XCD takes a contiguous piece of that order, so that the tiles an XCD works
 // on at one time share rows in its L2.
 constexpr int kGroup = 4;
-__device__ __forceinline__ void tile_of(const DenseArgs& a, int& nt, int& tt) {
+__device__ __forceinline__ void tile_of(const DenseArgs& a, int number, int& nt, int& tt) {
   const int items = a.n_nt * a.n_tt;
-  const int xcd = (int)blockIdx.x % kXcds, idx = (int)blockIdx.x / kXcds;
+  const int xcd = number % kXcds, idx = number / kXcds;
   const int q = items / kXcds, r = items % kXcds;
   const int item = xcd * q + min(xcd, r) + idx;
   const int group = item / (kGroup * a.n_tt);
@@ -122,6 +128,12 @@ struct Tile {
   static constexpr int kWaves = WN * WT;                // that multiply; NP more load
   static constexpr int kThreads = 64 * (kWaves + NP);
   static constexpr int TN = 16 * FA * WN, TT = 16 * FB * WT;
+  // The workgroups of large tiles, of which a CU holds one, stay and take one
+  // tile after the other: the next tile's loads run while the last one's
+  // results are stored.  21000 tokens: 4096 x 1024 weights 107 us (128 with a
+  // workgroup a tile), 8192 x 2048 365 (430), 4096 x 4096 325 (342).  Smaller
+  // tiles overlap with the CU's other workgroup, and gain nothing.
+  static constexpr bool kPersistent = TN * TT >= 128 * 128;
   static constexpr int kLoadsA = TN / 8 / NP, kLoadsB = TT / 8 / NP;  // 1 KB each
   static_assert(kFp8Block % (16 * FA) == 0, "a wave's weight rows lie in one scale block");
   static_assert(TN % (8 * NP) == 0 && TT % (8 * NP) == 0, "whole loads");
@@ -138,14 +150,60 @@ struct Tile {
   }
   static __device__ __forceinline__ bool gated_up(int r) { return (r % (16 * FA)) >= 8 * FA; }
 
+  // Where a tile lies: first weight row (gated: first H column) and token, and
+  // how many of them are inside the matrices.
+  struct Place {
+    int n0, n_live, t_live;
+    int64_t t0;
+  };
+  static __device__ __forceinline__ Place place(const DenseArgs& a, int number) {
+    constexpr int COLS = GATED ? TN / 2 : TN;
+    int nt, tt;
+    tile_of(a, number, nt, tt);
+    Place p;
+    p.n0 = nt * COLS;
+    p.t0 = (int64_t)tt * TT;
+    p.n_live = min(COLS, a.N - p.n0);
+    p.t_live = (int)min((int64_t)TT, a.T - p.t0);
+    return p;
+  }
+
   // What a wave loads: the tile's buffers (weight rows, gated: the up rows,
   // tokens, scales; rows past the end lie past the buffer's records: their
   // loads return zeros), and the lane's byte offset in each of its pieces at
   // K step 0.  Only the step's start, in the scalar offset, changes.
   struct Source {
-    rsrc_t w, up, x, xs;
+    rsrc_t w, up, x;
     int vw[kLoadsA], vx[kLoadsB];
   };
+  // The place of a lane's piece j within the step.
+  static __device__ __forceinline__ int row_in_tile(int piece, int lane) { return 8 * piece + (lane >> 3); }
+  static __device__ __forceinline__ int chunk_in_step(int row, int lane) { return ((lane & 7) ^ swz(row)) << 4; }
+  static __device__ __forceinline__ void open(Source& src, const DenseArgs& a, const Place& at, int wave, int lane) {
+    const int K = a.K;
+    src.w = make_rsrc(a.w + (int64_t)at.n0 * K, (uint32_t)at.n_live * K);
+    src.up = GATED ? make_rsrc(a.w + ((int64_t)a.N + at.n0) * K, (uint32_t)at.n_live * K) : src.w;
+    src.x = make_rsrc(a.x + at.t0 * K, (uint32_t)at.t_live * K);
+#pragma unroll
+    for (int j = 0; j < kLoadsA; ++j) {
+      const int r = row_in_tile(wave * kLoadsA + j, lane), row = GATED ? gated_col(r) : r;
+      src.vw[j] = row < at.n_live ? row * K + chunk_in_step(r, lane) : kOutOfRange;
+    }
+#pragma unroll
+    for (int j = 0; j < kLoadsB; ++j) {
+      const int r = row_in_tile(wave * kLoadsB + j, lane);
+      src.vx[j] = r < at.t_live ? r * K + chunk_in_step(r, lane) : kOutOfRange;
+    }
+  }
+  // Chunks at or past `end` of the coming step read as zeros, and so do all later ones.
+  static __device__ __forceinline__ void cut(Source& src, int end, int wave, int lane) {
+#pragma unroll
+    for (int j = 0; j < kLoadsA; ++j)
+      if (chunk_in_step(row_in_tile(wave * kLoadsA + j, lane), lane) >= end) src.vw[j] = kOutOfRange;
+#pragma unroll
+    for (int j = 0; j < kLoadsB; ++j)
+      if (chunk_in_step(row_in_tile(wave * kLoadsB + j, lane), lane) >= end) src.vx[j] = kOutOfRange;
+  }
   // The wave's j-th direct load of a K step into LDS: weight rows, then tokens.
   static constexpr int kLoads = kLoadsA + kLoadsB;
   static __device__ __forceinline__ void load_piece(int j, const Source& src, uint8_t* As, uint8_t* Bs, int k0,
@@ -161,8 +219,17 @@ struct Tile {
     }
   }
 
-  static __device__ __forceinline__ void load_16(rsrc_t r, void* lds, int v) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, v, 0, 0, 0);
+  // The scales of a run of steps: one load for 64 tokens, a lane takes its
+  // token's 16 bytes (values past a row's end are not used).
+  static __device__ __forceinline__ rsrc_t open_scales(const DenseArgs& a, const Place& at) {
+    return make_rsrc(a.xs + at.t0 * a.nb, (uint32_t)at.t_live * a.nb * 4);
+  }
+  static __device__ __forceinline__ void load_scales(rsrc_t xs, int nb, int run, float* to, int wave, int lane) {
+#pragma unroll
+    for (int q = 0; q < TT / 64; ++q)
+      if (q % NP == wave)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(xs, (lds_void*)(to + q * 64 * kScaleSteps), 16,
+                                                 ((q * 64 + lane) * nb + run * kScaleSteps) * 4, 0, 0, 0);
   }
 
   // LDS offset of chunk g of lane (r, g)'s row in a tile's first fragment.
@@ -218,6 +285,14 @@ struct Tile {
     float s[kSides][FB], s_last[kSides][FB];  // of this step, and of the one before
     v4f p[kLag + 1];
   };
+  static __device__ __forceinline__ void start(State& st) {
+#pragma unroll
+    for (int q = 0; q <= kLag; ++q) st.p[q] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kSides; ++k)
+#pragma unroll
+      for (int j = 0; j < FB; ++j) st.s[k][j] = st.s_last[k][j] = 0.f;
+  }
   static __device__ __forceinline__ void scales(State& st, const float* sx, float sw0, float sw1) {
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
@@ -276,268 +351,290 @@ __global__ __launch_bounds__(64 * (WN * WT + NP)) void k_dense_fp8(const DenseAr
   constexpr int TN = D::TN, TT = D::TT;
   constexpr bool GATED = D::GATED;
   __shared__ __align__(16) uint8_t As[STAGES * TN * kStep], Bs[STAGES * TT * kStep];
-  __shared__ __align__(16) float sxs[2 * TT * kScaleSteps];  // two runs of [token][step]
-  __shared__ float part[MODE == kGated ? WN : 1][MODE == kGated ? TT : 1];  // largest |H| of a token in a wave's columns
+  __shared__ __align__(16) float sxs[kRunBuffers * TT * kScaleSteps];  // runs of [token][step]
+  constexpr int PARTS = MODE == kGated ? WN : 1;
+  __shared__ float part[PARTS][MODE == kGated ? TT : 1];  // largest |H| of a token in a wave's columns
 
-  int nt, tt;
-  tile_of(a, nt, tt);
   const int K = a.K, nb = a.nb;
-  const int n0 = nt * (GATED ? TN / 2 : TN);  // first weight row (gated: first H column)
-  const int64_t t0 = (int64_t)tt * TT;
-  const int n_live = min(GATED ? TN / 2 : TN, a.N - n0);
-  const int t_live = (int)min((int64_t)TT, a.T - t0);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = wave % WN, wt = wave / WN;
+  const int first = (int)blockIdx.x;
+  const int stride = D::kPersistent ? (int)gridDim.x : 1, items = D::kPersistent ? a.n_nt * a.n_tt : first + 1;
 
   if (wave >= D::kWaves) {
-    // ---- loads ----
+    // ---- loads: the steps of all the workgroup's tiles in a row ----
     const int p = wave - D::kWaves;
+    const int tail = K % kStep ? K % kStep : kStep, runs = (nb + kScaleSteps - 1) / kScaleSteps;
     typename D::Source src;
-    src.w = make_rsrc(a.w + (int64_t)n0 * K, (uint32_t)n_live * K);
-    src.up = GATED ? make_rsrc(a.w + ((int64_t)a.N + n0) * K, (uint32_t)n_live * K) : src.w;
-    src.x = make_rsrc(a.x + t0 * K, (uint32_t)t_live * K);
-    src.xs = make_rsrc(a.xs + t0 * nb, (uint32_t)t_live * nb * 4);
-    int cw[D::kLoadsA], cx[D::kLoadsB];  // the pieces' places within the step
-#pragma unroll
-    for (int j = 0; j < D::kLoadsA; ++j) {
-      const int r = 8 * (p * D::kLoadsA + j) + (lane >> 3);
-      const int row = GATED ? D::gated_col(r) : r;
-      cw[j] = ((lane & 7) ^ swz(r)) << 4;
-      src.vw[j] = row < n_live ? row * K + cw[j] : kOutOfRange;
-    }
-#pragma unroll
-    for (int j = 0; j < D::kLoadsB; ++j) {
-      const int r = 8 * (p * D::kLoadsB + j) + (lane >> 3);
-      cx[j] = ((lane & 7) ^ swz(r)) << 4;
-      src.vx[j] = r < t_live ? r * K + cx[j] : kOutOfRange;
-    }
-    // the last step of a ragged K: chunks past the row's end read as zeros; past
-    // the last step nothing is read (the zeros go to buffers no step uses)
-    const int tail = K % kStep ? K % kStep : kStep;
-    auto cut = [&](int step) {
-      const int end = step >= nb ? 0 : step == nb - 1 ? tail : kStep;
-      if (end < kStep) {
-#pragma unroll
-        for (int j = 0; j < D::kLoadsA; ++j)
-          if (cw[j] >= end) src.vw[j] = kOutOfRange;
-#pragma unroll
-        for (int j = 0; j < D::kLoadsB; ++j)
-          if (cx[j] >= end) src.vx[j] = kOutOfRange;
+    int tile = first, step = 0, buf = 0;  // what is loaded next
+    const typename D::Place at = D::place(a, tile);
+    D::open(src, a, at, p, lane);
+    // past the last tile nothing is read (the zeros go to buffers no step uses)
+    auto prepare = [&]() {
+      if constexpr (D::kPersistent) {
+        if (step == nb) {
+          step = 0;
+          tile = tile < items ? tile + stride : tile;
+          if (tile < items) D::open(src, a, D::place(a, tile), p, lane);
+        }
       }
+      const int end = tile >= items || step >= nb ? 0 : step == nb - 1 ? tail : kStep;
+      if (end < kStep) D::cut(src, end, p, lane);
     };
-    auto load_step = [&](int step, int buf) {
-      cut(step);
+    auto load_next = [&]() {
 #pragma unroll
       for (int j = 0; j < D::kLoads; ++j)
         D::load_piece(j, src, As + buf * TN * kStep, Bs + buf * TT * kStep, step * kStep, p);
+      ++step;
+      buf = buf + 1 == STAGES ? 0 : buf + 1;
     };
-    // a run's scales: one load for 64 tokens, a lane takes its token's 16 bytes
-    auto load_scales = [&](int run) {
-#pragma unroll
-      for (int q = 0; q < TT / 64; ++q)
-        if (q % NP == p)
-          D::load_16(src.xs, sxs + ((run & 1) * TT + q * 64) * kScaleSteps, ((q * 64 + lane) * nb + run * kScaleSteps) * 4);
+    int run_tile = first, run = 0, run_buf = 0;
+    rsrc_t xs = D::open_scales(a, at);
+    auto load_next_run = [&]() {
+      if constexpr (D::kPersistent) {
+        if (run == runs) {
+          run = 0;
+          run_tile = run_tile < items ? run_tile + stride : run_tile;
+          if (run_tile < items) xs = D::open_scales(a, D::place(a, run_tile));
+        }
+      }
+      if (run_tile < items && run < runs) D::load_scales(xs, nb, run, sxs + run_buf * TT * kScaleSteps, p, lane);
+      ++run;
+      run_buf = run_buf + 1 == kRunBuffers ? 0 : run_buf + 1;
     };
     // Fragments are read a step ahead: at barrier s step s + 1 has landed and
-    // the buffers of step s are free.
-    load_scales(0);
+    // the buffers of step s are free.  A run's scales are loaded when the third
+    // run before it begins: whatever the runs' lengths, three barriers or more
+    // lie between, which wait for all but the loads of the last steps, and the
+    // buffer's last reader is done.
 #pragma unroll
-    for (int s = 0; s < STAGES; ++s) load_step(s, s);
+    for (int r = 0; r < kRunBuffers - 1; ++r) load_next_run();
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) {
+      prepare();
+      load_next();
+    }
     loads_done_barrier<(STAGES - 1) * D::kLoads>();
-    int next = 0;
 #pragma unroll 1
-    for (int s = 0; s < nb; ++s) {
-      loads_done_barrier<(STAGES - 2) * D::kLoads>();
-      if ((s & (kScaleSteps - 1)) == 0 && s + kScaleSteps < nb) load_scales(s / kScaleSteps + 1);
-      load_step(s + STAGES, next);
-      next = next + 1 == STAGES ? 0 : next + 1;
+    for (int i = first; i < items; i += stride) {
+#pragma unroll 1
+      for (int s = 0; s < nb; ++s) {
+        prepare();
+        asm volatile("" : "+s"(step), "+s"(buf));  // before the barrier, where these waves wait
+        loads_done_barrier<(STAGES - 2) * D::kLoads>();
+        if ((s & (kScaleSteps - 1)) == 0) load_next_run();
+        load_next();
+      }
+      if (MODE == kGated) lds_barrier();
     }
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no load may still write LDS when the workgroup ends
-    if (MODE == kGated) lds_barrier();
     return;
   }
   // ---- products ----
+  const int wn = wave % WN, wt = wave / WN;
   // weight scales: one for the wave's rows and step (gated: one of the gate
   // rows, one of the up rows), a step ahead in scalar registers
   const int nbn = (a.N + kFp8Block - 1) / kFp8Block;
-  const int blk = GATED ? n0 / kFp8Block : min((n0 + wn * 16 * FA) / kFp8Block, nbn - 1);
   typedef const __attribute__((address_space(4))) float* const_floats;
-  const const_floats ws0 = (const_floats)(a.ws + (int64_t)blk * nb);
-  const const_floats ws1 = (const_floats)(a.ws + (int64_t)(blk + (GATED ? nbn : 0)) * nb);
-  v4f acc[FA][FB] = {};
-  typename D::State st = {};
+  auto weight_scales = [&](int n0) {
+    const int block = GATED ? n0 / kFp8Block : min((n0 + wn * 16 * FA) / kFp8Block, nbn - 1);
+    return (const_floats)(a.ws + (int64_t)block * nb);
+  };
+  const int64_t up = GATED ? (int64_t)nbn * nb : 0;
+  typename D::State st;
   const int a_off = D::lane_offset(wn * 16 * FA + (lane & 15), lane >> 4);
   const int b_off = D::lane_offset(wt * 16 * FB + (lane & 15), lane >> 4);
   const float* sx = sxs + (wt * 16 * FB + (lane & 15)) * kScaleSteps;
+  typename D::Place at = D::place(a, first);
+  const_floats ws = weight_scales(at.n0);
+  const_floats ws1 = ws + up;
+  float sw0 = ws[0], sw1 = ws1[0];
   loads_done_barrier<63>();  // step 0 has landed
 #pragma unroll
   for (int i = 0; i < FA; ++i) st.a[i] = D::fragment(As + a_off, As + (a_off ^ 64), i);
 #pragma unroll
   for (int j = 0; j < FB; ++j) st.b[j] = D::fragment(Bs + b_off, Bs + (b_off ^ 64), j);
-  int cur = 1;
-  float sw0 = ws0[0], sw1 = ws1[0];
+  int cur = 1;           // the coming step's buffers
+  uint32_t in_runs = 0;  // and its place in the runs of scales, each of which starts at a multiple of kScaleSteps
 #pragma unroll 1
-  for (int s = 0; s < nb; ++s) {
-    loads_done_barrier<63>();
-    D::scales(st, sx + ((s >> kScaleShift) & 1) * TT * kScaleSteps + (s & (kScaleSteps - 1)), sw0, sw1);
-    const int ahead = min(s + 1, nb - 1);
-    sw0 = ws0[ahead];
-    sw1 = ws1[ahead];
-    const int al = cur * TN * kStep + a_off, bl = cur * TT * kStep + b_off;
-    D::multiply(st, As + al, As + (al ^ 64), Bs + bl, Bs + (bl ^ 64), acc);
-    cur = cur + 1 == STAGES ? 0 : cur + 1;
-  }
-  D::finish(st, acc);
+  for (int tile = first; tile < items; tile += stride) {
+    v4f acc[FA][FB] = {};
+    D::start(st);
+#pragma unroll 1
+    for (int s = 0; s < nb;) {
+      loads_done_barrier<63>();
+      D::scales(st, sx + (in_runs / kScaleSteps % kRunBuffers * (TT * kScaleSteps) + in_runs % kScaleSteps), sw0, sw1);
+      const int al = cur * TN * kStep + a_off, bl = cur * TT * kStep + b_off;
+      D::multiply(st, As + al, As + (al ^ 64), Bs + bl, Bs + (bl ^ 64), acc);
+      ++s;
+      const uint32_t ahead = (uint32_t)min(s, nb - 1);
+      sw0 = ws[ahead];
+      if (GATED) sw1 = ws1[ahead];
+      cur = cur + 1 == STAGES ? 0 : cur + 1;
+      ++in_runs;
+      if (D::kPersistent && s == nb) in_runs = (in_runs + kScaleSteps - 1) / kScaleSteps * kScaleSteps;
+    }
+    D::finish(st, acc);
+    const int n0 = at.n0, n_live = at.n_live, t_live = at.t_live;
+    const int64_t t0 = at.t0;
+    if (tile + stride < items) {
+      at = D::place(a, tile + stride);
+      ws = weight_scales(at.n0);
+      ws1 = ws + up;
+      sw0 = ws[0];
+      sw1 = ws1[0];
+    }
 
-  const int r = lane & 15, g = lane >> 4;
-  if constexpr (MODE == kGatedRaw) {
+    const int r = lane & 15, g = lane >> 4;
+    if constexpr (MODE == kGatedRaw) {
 #pragma unroll
-    for (int j = 0; j < FB; ++j)
+      for (int j = 0; j < FB; ++j)
 #pragma unroll
-      for (int i = 0; i < FA / 2; ++i) {
-        const int tl = wt * 16 * FB + 16 * j + r, n = wn * 8 * FA + 16 * i + 4 * g;
-        v4f h;
+        for (int i = 0; i < FA / 2; ++i) {
+          const int tl = wt * 16 * FB + 16 * j + r, n = wn * 8 * FA + 16 * i + 4 * g;
+          v4f h;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = silu(acc[i][j][e]) * acc[i + FA / 2][j][e];
-        if (tl < t_live && n < n_live) *reinterpret_cast<v4f*>(a.y_f32 + (t0 + tl) * a.N + n0 + n) = h;
-      }
-  } else if constexpr (!GATED) {
-    const bool vec4 = a.N % 4 == 0, vec8 = a.N % 8 == 0;
+          for (int e = 0; e < 4; ++e) h[e] = silu(acc[i][j][e]) * acc[i + FA / 2][j][e];
+          if (tl < t_live && n < n_live) *reinterpret_cast<v4f*>(a.y_f32 + (t0 + tl) * a.N + n0 + n) = h;
+        }
+    } else if constexpr (!GATED) {
+      const bool vec4 = a.N % 4 == 0, vec8 = a.N % 8 == 0;
 #pragma unroll
-    for (int j = 0; j < FB; ++j) {
-      const int tl = wt * 16 * FB + 16 * j + r;
-      const bool live = tl < t_live;
-      const int64_t t = t0 + tl;
-      if (a.y_f32) {
+      for (int j = 0; j < FB; ++j) {
+        const int tl = wt * 16 * FB + 16 * j + r;
+        const bool live = tl < t_live;
+        const int64_t t = t0 + tl;
+        if (a.y_f32) {
 #pragma unroll
-        for (int i = 0; i < FA; ++i) {
-          const int n = n0 + wn * 16 * FA + 16 * i + 4 * g;
-          const v4f v = acc[i][j];
-          if (live && n < a.N) {
-            float* dst = a.y_f32 + t * a.N + n;
-            if (vec4) *reinterpret_cast<v4f*>(dst) = v;
-            else
-              for (int e = 0; e < 4; ++e)
-                if (n + e < a.N) dst[e] = v[e];
+          for (int i = 0; i < FA; ++i) {
+            const int n = n0 + wn * 16 * FA + 16 * i + 4 * g;
+            const v4f v = acc[i][j];
+            if (live && n < a.N) {
+              float* dst = a.y_f32 + t * a.N + n;
+              if (vec4) *reinterpret_cast<v4f*>(dst) = v;
+              else
+                for (int e = 0; e < 4; ++e)
+                  if (n + e < a.N) dst[e] = v[e];
+            }
           }
         }
-      }
-      if (a.y_bf16) {
-        // four fragments at a time (a narrow tile has two, and the other half
-        // of the lanes nothing to store), transposed among the lane groups: a
-        // lane then stores 16 neighbouring columns
+        if (a.y_bf16) {
+          // four fragments at a time (a narrow tile has two, and the other half
+          // of the lanes nothing to store), transposed among the lane groups: a
+          // lane then stores 16 neighbouring columns
 #pragma unroll
-        for (int q = 0; q < FA; q += 4) {
-          uint32_t lo[4], hi[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const v4f v = acc[q + i < FA ? q + i : q][j];
-            lo[i] = pack_bf16(v[0], v[1]);
-            hi[i] = pack_bf16(v[2], v[3]);
-          }
-          transpose4(lo);
-          transpose4(hi);
-          const int n = n0 + wn * 16 * FA + 16 * (q + g);
-          uint16_t* dst = a.y_bf16 + t * a.N + n;
-          if (!live || q + g >= FA) continue;
-          if (vec8) {
-            if (n < a.N) *reinterpret_cast<uint4*>(dst) = uint4{lo[0], hi[0], lo[1], hi[1]};
-            if (n + 8 < a.N) *reinterpret_cast<uint4*>(dst + 8) = uint4{lo[2], hi[2], lo[3], hi[3]};
-          } else {
+          for (int q = 0; q < FA; q += 4) {
+            uint32_t lo[4], hi[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if (vec4) {
-                if (n + 4 * i < a.N) *reinterpret_cast<uint2*>(dst + 4 * i) = uint2{lo[i], hi[i]};
-              } else {
-                for (int e = 0; e < 4; ++e)
-                  if (n + 4 * i + e < a.N) dst[4 * i + e] = (uint16_t)((e < 2 ? lo[i] : hi[i]) >> (16 * (e & 1)));
+              const v4f v = acc[q + i < FA ? q + i : q][j];
+              lo[i] = pack_bf16(v[0], v[1]);
+              hi[i] = pack_bf16(v[2], v[3]);
+            }
+            transpose4(lo);
+            transpose4(hi);
+            const int n = n0 + wn * 16 * FA + 16 * (q + g);
+            uint16_t* dst = a.y_bf16 + t * a.N + n;
+            if (!live || q + g >= FA) continue;
+            if (vec8) {
+              if (n < a.N) *reinterpret_cast<uint4*>(dst) = uint4{lo[0], hi[0], lo[1], hi[1]};
+              if (n + 8 < a.N) *reinterpret_cast<uint4*>(dst + 8) = uint4{lo[2], hi[2], lo[3], hi[3]};
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (vec4) {
+                  if (n + 4 * i < a.N) *reinterpret_cast<uint2*>(dst + 4 * i) = uint2{lo[i], hi[i]};
+                } else {
+                  for (int e = 0; e < 4; ++e)
+                    if (n + 4 * i + e < a.N)
+                      dst[4 * i + e] = (uint16_t)((e < 2 ? lo[i] : hi[i]) >> (16 * (e & 1)));
+                }
               }
             }
           }
         }
-      }
-      if (a.y_q8) {
+        if (a.y_q8) {
 #pragma clang fp contract(off)
-        // fragments 2q and 2q + 1 are one q8_1 block of the token
+          // fragments 2q and 2q + 1 are one q8_1 block of the token
 #pragma unroll
-        for (int q = 0; q < FA / 2; ++q) {
-          const int n = n0 + wn * 16 * FA + 32 * q;
-          float amax = 0.f;
+          for (int q = 0; q < FA / 2; ++q) {
+            const int n = n0 + wn * 16 * FA + 32 * q;
+            float amax = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            amax = fmaxf(amax, fmaxf(fabsf(acc[2 * q][j][e]), fabsf(acc[2 * q + 1][j][e])));
-          amax = fmaxf(amax, __shfl_xor(amax, 16));
-          amax = fmaxf(amax, __shfl_xor(amax, 32));
-          const float d = amax / 127.0f;
-          const float id = d != 0.0f ? 1.0f / d : 0.0f;
-          uint32_t pk[2];
-          int sum = 0;
+            for (int e = 0; e < 4; ++e)
+              amax = fmaxf(amax, fmaxf(fabsf(acc[2 * q][j][e]), fabsf(acc[2 * q + 1][j][e])));
+            amax = fmaxf(amax, __shfl_xor(amax, 16));
+            amax = fmaxf(amax, __shfl_xor(amax, 32));
+            const float d = amax / 127.0f;
+            const float id = d != 0.0f ? 1.0f / d : 0.0f;
+            uint32_t pk[2];
+            int sum = 0;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const v4f v = acc[2 * q + h][j];
-            pk[h] = pack_codes(round_half_away(v[0] * id), round_half_away(v[1] * id), round_half_away(v[2] * id),
-                               round_half_away(v[3] * id));
-            sum = __builtin_amdgcn_sdot4((int)pk[h], 0x01010101, sum, false);
-          }
-          sum += __shfl_xor(sum, 16);
-          sum += __shfl_xor(sum, 32);
-          if (live && n < a.N) {
-            uint32_t* blk = reinterpret_cast<uint32_t*>(a.y_q8 + (t * (a.N / 32) + n / 32) * kQ81Bytes);
-            blk[1 + g] = pk[0];
-            blk[5 + g] = pk[1];
-            if (g == 0) blk[0] = float_to_half_bits(d) | (float_to_half_bits(fp32_barrier(d * (float)sum)) << 16);
+            for (int h = 0; h < 2; ++h) {
+              const v4f v = acc[2 * q + h][j];
+              pk[h] = pack_codes(round_half_away(v[0] * id), round_half_away(v[1] * id), round_half_away(v[2] * id),
+                                 round_half_away(v[3] * id));
+              sum = __builtin_amdgcn_sdot4((int)pk[h], 0x01010101, sum, false);
+            }
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (live && n < a.N) {
+              uint32_t* blk = reinterpret_cast<uint32_t*>(a.y_q8 + (t * (a.N / 32) + n / 32) * kQ81Bytes);
+              blk[1 + g] = pk[0];
+              blk[5 + g] = pk[1];
+              if (g == 0) blk[0] = float_to_half_bits(d) | (float_to_half_bits(fp32_barrier(d * (float)sum)) << 16);
+            }
           }
         }
       }
-    }
-  } else {
-    // H = silu(G) U in place of the gate accumulators; a token's 128 columns
-    // of the tile are one e4m3 block, held by WN waves
+    } else {
+      // H = silu(G) U in place of the gate accumulators; a token's 128 columns
+      // of the tile are one e4m3 block, held by WN waves
 #pragma unroll
-    for (int j = 0; j < FB; ++j) {
-      float amax = 0.f;
+      for (int j = 0; j < FB; ++j) {
+        float amax = 0.f;
 #pragma unroll
-      for (int i = 0; i < FA / 2; ++i)
+        for (int i = 0; i < FA / 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float h = silu(acc[i][j][e]) * acc[i + FA / 2][j][e];
-          acc[i][j][e] = h;
-          amax = fmaxf(amax, fabsf(h));
-        }
-      amax = fmaxf(amax, __shfl_xor(amax, 16));
-      amax = fmaxf(amax, __shfl_xor(amax, 32));
-      if (g == 0) part[wn][wt * 16 * FB + 16 * j + r] = amax;
-    }
-    lds_barrier();
-    const int hb = (a.N + kFp8Block - 1) / kFp8Block;
-#pragma unroll
-    for (int j = 0; j < FB; ++j) {
-#pragma clang fp contract(off)
-      const int tl = wt * 16 * FB + 16 * j + r;
-      float amax = part[0][tl];
-#pragma unroll
-      for (int w = 1; w < WN; ++w) amax = fmaxf(amax, part[w][tl]);
-      float id;
-      const float scale = fp8_scale(amax, id);
-      const int64_t t = t0 + tl;
-      if (tl < t_live && wn == 0 && g == 0) a.hs[t * hb + n0 / kFp8Block] = scale;
-      uint32_t pk[FA / 2];
-#pragma unroll
-      for (int i = 0; i < FA / 2; ++i) {
-        const v4f v = acc[i][j];
-        pk[i] = pack_e4m3(v[0] * id, v[1] * id, v[2] * id, v[3] * id);
+          for (int e = 0; e < 4; ++e) {
+            const float h = silu(acc[i][j][e]) * acc[i + FA / 2][j][e];
+            acc[i][j][e] = h;
+            amax = fmaxf(amax, fabsf(h));
+          }
+        amax = fmaxf(amax, __shfl_xor(amax, 16));
+        amax = fmaxf(amax, __shfl_xor(amax, 32));
+        if (g == 0) part[wn][wt * 16 * FB + 16 * j + r] = amax;
       }
-      if constexpr (FA == 8) {  // a lane stores 16 neighbouring columns
-        transpose4(pk);
-        const int n = wn * 64 + 16 * g;
-        if (tl < t_live && n < n_live)
-          *reinterpret_cast<uint4*>(a.h + t * a.N + n0 + n) = uint4{pk[0], pk[1], pk[2], pk[3]};
-      } else {
+      lds_barrier();
+      const int hb = (a.N + kFp8Block - 1) / kFp8Block;
+#pragma unroll
+      for (int j = 0; j < FB; ++j) {
+#pragma clang fp contract(off)
+        const int tl = wt * 16 * FB + 16 * j + r;
+        float amax = part[0][tl];
+#pragma unroll
+        for (int w = 1; w < WN; ++w) amax = fmaxf(amax, part[w][tl]);
+        float id;
+        const float scale = fp8_scale(amax, id);
+        const int64_t t = t0 + tl;
+        if (tl < t_live && wn == 0 && g == 0) a.hs[t * hb + n0 / kFp8Block] = scale;
+        uint32_t pk[FA / 2];
 #pragma unroll
         for (int i = 0; i < FA / 2; ++i) {
-          const int n = wn * 8 * FA + 16 * i + 4 * g;
-          if (tl < t_live && n < n_live) *reinterpret_cast<uint32_t*>(a.h + t * a.N + n0 + n) = pk[i];
+          const v4f v = acc[i][j];
+          pk[i] = pack_e4m3(v[0] * id, v[1] * id, v[2] * id, v[3] * id);
+        }
+        if constexpr (FA == 8) {  // a lane stores 16 neighbouring columns
+          transpose4(pk);
+          const int n = wn * 64 + 16 * g;
+          if (tl < t_live && n < n_live)
+            *reinterpret_cast<uint4*>(a.h + t * a.N + n0 + n) = uint4{pk[0], pk[1], pk[2], pk[3]};
+        } else {
+#pragma unroll
+          for (int i = 0; i < FA / 2; ++i) {
+            const int n = wn * 8 * FA + 16 * i + 4 * g;
+            if (tl < t_live && n < n_live) *reinterpret_cast<uint32_t*>(a.h + t * a.N + n0 + n) = pk[i];
+          }
         }
       }
     }
@@ -545,13 +642,14 @@ __global__ __launch_bounds__(64 * (WN * WT + NP)) void k_dense_fp8(const DenseAr
 }
 
 template <int FA, int FB, int WN, int WT, int MODE, int STAGES, int NP>
-hipError_t run(DenseArgs a, hipStream_t st) {
+hipError_t run(DenseArgs a, int num_cus, hipStream_t st) {
   using D = Tile<FA, FB, WN, WT, MODE, STAGES, NP>;
   const int tn = D::GATED ? D::TN / 2 : D::TN;
   a.n_nt = (a.N + tn - 1) / tn;
   a.n_tt = (int)((a.T + D::TT - 1) / D::TT);
-  hipLaunchKernelGGL((k_dense_fp8<FA, FB, WN, WT, MODE, STAGES, NP>), dim3((unsigned)(a.n_nt * a.n_tt)), dim3(D::kThreads),
-                     0, st, a);
+  const int items = a.n_nt * a.n_tt, grid = D::kPersistent ? std::min(items, num_cus) : items;
+  hipLaunchKernelGGL((k_dense_fp8<FA, FB, WN, WT, MODE, STAGES, NP>), dim3((unsigned)grid), dim3(D::kThreads), 0, st,
+                     a);
   return hipGetLastError();
 }
 
@@ -559,22 +657,25 @@ hipError_t run(DenseArgs a, hipStream_t st) {
 // small ones fill the chip with few rows and leave less of its last pass idle.
 // The time of a variant is estimated from what one CU was measured to take for
 // a K step while it holds 1, 2, ... of the variant's tiles (us; the launch has
-// 256 CUs busy) and for what a tile costs beside its steps: passes with every
-// CU full, then one with the tiles that remain.
+// 256 CUs busy), for what a tile costs beside its steps, and for the start:
+// passes with every CU full, then one with the tiles that remain.
 struct Variant {
   int cols, tokens;  // of a tile
   int per_cu;        // tiles a CU holds (LDS)
-  float fixed, step[4];
+  float start, tile, step[2];
 };
-constexpr Variant kFastTiles[] = {{256, 128, 1, 6.f, {0.86f}},
-                                  {128, 128, 1, 5.f, {0.46f}},
-                                  {128, 64, 2, 4.f, {0.32f, 0.65f}},
-                                  {64, 64, 2, 3.f, {0.20f, 0.39f}}};
-constexpr Variant kExactTiles[] = {
-    {128, 192, 1, 7.f, {1.42f}}, {128, 128, 1, 6.f, {0.92f}}, {64, 64, 2, 4.f, {0.35f, 0.57f}}};
-constexpr Variant kGatedTiles[] = {{128, 128, 1, 7.f, {0.86f}}, {128, 64, 1, 5.f, {0.50f}},
+constexpr Variant kFastTiles[] = {{256, 128, 1, 3.f, 3.f, {0.86f}},
+                                  {128, 128, 1, 3.f, 2.f, {0.46f}},
+                                  {128, 64, 2, 0.f, 4.f, {0.32f, 0.65f}},
+                                  {64, 64, 2, 0.f, 3.f, {0.20f, 0.39f}}};
+constexpr Variant kExactTiles[] = {{128, 192, 1, 5.f, 2.f, {1.40f}},
+                                   {128, 128, 1, 4.f, 2.f, {0.92f}},
+                                   {64, 64, 2, 0.f, 4.f, {0.35f, 0.57f}}};
+constexpr Variant kGatedTiles[] = {{128, 128, 1, 4.f, 3.f, {0.86f}},
+                                   {128, 64, 1, 3.f, 2.f, {0.50f}},
                                    // with the rounding in a launch of its own
-                                   {64, 64, 2, 7.f, {0.32f, 0.65f}}, {32, 64, 2, 6.f, {0.20f, 0.39f}}};
+                                   {64, 64, 2, 3.f, 4.f, {0.32f, 0.65f}},
+                                   {32, 64, 2, 3.f, 3.f, {0.20f, 0.39f}}};
 // Variants that round H themselves.  128 columns of H are one scale's, so these
 // fill the chip only where T F is large: 65 tokens of C = 4096, F = 2048 (16
 // tiles of 128 x 64) took 24.0 us for the whole block, and take 16.9 us with
@@ -587,8 +688,8 @@ int pick(const Variant* v, int count, int64_t T, int N, int nb, int num_cus) {
   for (int i = 0; i < count; ++i) {
     const int64_t tiles = ((T + v[i].tokens - 1) / v[i].tokens) * ((N + v[i].cols - 1) / v[i].cols);
     const int64_t slots = (int64_t)num_cus * v[i].per_cu, passes = tiles / slots, rest = tiles % slots;
-    float t = (float)passes * (v[i].step[v[i].per_cu - 1] * (float)nb + v[i].fixed);
-    if (rest) t += v[i].step[(rest + num_cus - 1) / num_cus - 1] * (float)nb + v[i].fixed;
+    float t = v[i].start + (float)passes * (v[i].step[v[i].per_cu - 1] * (float)nb + v[i].tile);
+    if (rest) t += v[i].step[(rest + num_cus - 1) / num_cus - 1] * (float)nb + v[i].tile;
     if (i == 0 || t < least) {
       best = i;
       least = t;
@@ -604,27 +705,28 @@ hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w,
   const DenseArgs a{x, xs, w, ws, y_f32, y_bf16, y_q8, nullptr, nullptr, T, N, K, (K + kStep - 1) / kStep, 0, 0};
   if (y_f32) {  // exact products (see the head of the file)
     switch (pick(kExactTiles, 3, T, N, a.nb, num_cus)) {
-      case 0: return run<4, 3, 2, 4, kExact, 3, 4>(a, st);
-      case 1: return run<4, 4, 2, 2, kExact, 3, 2>(a, st);
-      default: return run<2, 2, 2, 2, kExact, 4, 4>(a, st);
+      case 0: return run<4, 3, 2, 4, kExact, 3, 4>(a, num_cus, st);
+      case 1: return run<4, 4, 2, 2, kExact, 3, 2>(a, num_cus, st);
+      default: return run<2, 2, 2, 2, kExact, 4, 4>(a, num_cus, st);
     }
   }
   switch (pick(kFastTiles, 4, T, N, a.nb, num_cus)) {
-    case 0: return run<4, 4, 4, 2, kFast, 3, 4>(a, st);
-    case 1: return run<4, 4, 2, 2, kFast, 3, 4>(a, st);
-    case 2: return run<4, 2, 2, 2, kFast, 3, 2>(a, st);
-    default: return run<2, 2, 2, 2, kFast, 4, 4>(a, st);
+    case 0: return run<4, 4, 4, 2, kFast, 3, 4>(a, num_cus, st);
+    case 1: return run<4, 4, 2, 2, kFast, 3, 4>(a, num_cus, st);
+    case 2: return run<4, 2, 2, 2, kFast, 3, 2>(a, num_cus, st);
+    default: return run<2, 2, 2, 2, kFast, 4, 4>(a, num_cus, st);
   }
 }
 
 hipError_t launch_gateup_fp8(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int64_t T, int F,
                              int C, float* h32, uint8_t* h, float* hs, int num_cus, hipStream_t st) {
   const DenseArgs a{x, xs, gu, gus, h32, nullptr, nullptr, h, hs, T, F, C, (C + kStep - 1) / kStep, 0, 0};
-  const int variant = pick(kGatedTiles, T * F <= kFp8H32 ? 4 : kGatedRounded, T, F, a.nb, num_cus);
-  if (variant == 0) return run<4, 4, 4, 2, kGated, 3, 4>(a, st);
-  if (variant == 1) return run<8, 2, 2, 2, kGated, 3, 4>(a, st);
-  const hipError_t e =
-      variant == 2 ? run<4, 2, 2, 2, kGatedRaw, 3, 2>(a, st) : run<2, 2, 2, 2, kGatedRaw, 4, 4>(a, st);
+  const int choices = T * F <= kFp8H32 ? 4 : kGatedRounded;
+  const int variant = pick(kGatedTiles, choices, T, F, a.nb, num_cus);
+  if (variant == 0) return run<4, 4, 4, 2, kGated, 3, 4>(a, num_cus, st);
+  if (variant == 1) return run<8, 2, 2, 2, kGated, 3, 4>(a, num_cus, st);
+  const hipError_t e = variant == 2 ? run<4, 2, 2, 2, kGatedRaw, 3, 2>(a, num_cus, st)
+                                    : run<2, 2, 2, 2, kGatedRaw, 4, 4>(a, num_cus, st);
   return e == hipSuccess ? launch_quantize_fp8(h32, LAT_MOE_F32, T, F, h, hs, st) : e;
 }
 

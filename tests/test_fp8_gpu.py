@@ -106,7 +106,7 @@ def test_dense_matches_oracle(T, N, K):
 
 # many token and weight tiles: the tile order, and every variant's edges
 @pytest.mark.parametrize("T,N,K", [(2100, 544, 528), (5268, 1024, 256), (4133, 2052, 144), (700, 4096, 128), (9000, 96, 384),
-                                   (1500, 2070, 656), (2100, 2067, 528)])
+                                   (1500, 2070, 656), (2100, 2067, 528), (3000, 2068, 656)])
 def test_dense_of_many_tiles(T, N, K):
     rng = np.random.default_rng(T)
     (x, xs), (w, ws) = _x(rng, T, K), _w(rng, N, K)
@@ -133,7 +133,7 @@ def test_dense_of_few_tokens_does_not_depend_on_what_is_asked_for(T):
 @pytest.mark.parametrize("T,N,K", [(17, 288, 656), (65, 288, 656), (130, 1, 16), (300, 515, 2064), (2500, 96, 144),
                                    (700, 1060, 128), (5268, 260, 256), (700, 4112, 272), (2100, 1056, 144),
                                    (700, 4128, 656), (1500, 2070, 656), (1500, 4128, 272), (4133, 2052, 144),
-                                   (4133, 1025, 656)])
+                                   (4133, 1025, 656), (2100, 4112, 656), (9000, 2052, 128)])
 def test_dense_rounded_outputs_alone(T, N, K):
     rng = np.random.default_rng(T)
     (x, xs), (w, ws) = _x(rng, T, K), _w(rng, N, K)
@@ -221,7 +221,8 @@ def _ffn(args, T, C, F, h=True, f32=True):
 @pytest.mark.parametrize("T,C,F", [(T, C, F) for T in (1, 4, 16, 17, 64, 200, 2100)
                                    for C, F in ((16, 16), (128, 128), (400, 272), (1024, 512), (256, 1040), (2064, 144))]
                          + [(8, 128, 2064), (9, 128, 272), (700, 2064, 1040), (530, 2064, 1936), (700, 656, 272),
-                            (700, 272, 1040), (700, 272, 4112), (2100, 400, 2064), (5200, 144, 272)])
+                            (700, 272, 1040), (700, 272, 4112), (2100, 400, 2064), (5200, 144, 272),
+                            (9000, 144, 528), (6000, 144, 528), (2500, 656, 2576)])
 def test_ffn_matches_oracle_stage_by_stage(T, C, F):
     rng = np.random.default_rng(T + C + F)
     args = _ffn_inputs(rng, T, C, F)
