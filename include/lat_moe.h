@@ -333,7 +333,8 @@ int lat_moe_rmsnorm(const void* x, int32_t x_type, const void* residual, int32_t
  * same fp32 y.  Supported: T >= 0, T < 2^31, 1 <= N <= LAT_MOE_FP8_MAX_N, K % 16 == 0,
  * 16 <= K <= 65536, ceil(T/64) * ceil(N/64) < 2^31; pointers 16-byte aligned.
  * A code that is a NaN makes the outputs that it enters NaN and no others.
- * T = 0 enqueues nothing.  Outputs are deterministic.  No workspace. */
+ * Outputs must not overlap an input or each other.  T = 0 enqueues nothing.
+ * Outputs are deterministic.  No workspace. */
 int lat_moe_dense_fp8(const void* x_fp8, const float* x_scales, const void* w_fp8, const float* w_scales, int64_t T,
                       int32_t N, int32_t K, float* y_f32, void* y_bf16, void* y_q8_1, void* stream);
 
@@ -355,8 +356,10 @@ int lat_moe_dense_fp8(const void* x_fp8, const float* x_scales, const void* w_fp
  *                    no initialisation
  * Supported: T >= 0, T < 2^31, C % 16 == 0, F % 16 == 0, 16 <= C, F <= 65536,
  * 2F * C < 2^31, and at most 2^31 tiles of each product as above (the size is 0
- * for unsupported shapes).  Pointers 16-byte aligned.  T = 0 enqueues nothing.
- * Outputs are deterministic. */
+ * for unsupported shapes).  Pointers 16-byte aligned.  Outputs and the workspace
+ * must not overlap an input or each other; calls that may run at the same time
+ * need a workspace each.  The workspace size does not fall as T grows.  T = 0
+ * enqueues nothing.  Outputs are deterministic. */
 size_t lat_moe_ffn_fp8_workspace_size(int64_t T, int32_t C, int32_t F);
 int lat_moe_ffn_fp8(const void* x_fp8, const float* x_scales, const void* gateup_fp8, const float* gateup_scales,
                     const void* down_fp8, const float* down_scales, int64_t T, int32_t C, int32_t F, float* y_f32,

@@ -17,6 +17,14 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 
+// A launch has fewer than 2^32 threads along a dimension: more than 2^20
+// workgroups come in rows of 2^20, and those past the last one return at once.
+inline dim3 grid_of(int64_t workgroups) {
+  constexpr int64_t kRow = 1 << 20;
+  return workgroups <= kRow ? dim3((unsigned)workgroups) : dim3(kRow, (unsigned)((workgroups + kRow - 1) / kRow));
+}
+__device__ __forceinline__ uint32_t workgroup_number() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Scale of a block whose largest magnitude is amax, and what its values are
 // multiplied by to get the codes: two quotients of amax, each rounded once.
 __device__ __forceinline__ float fp8_scale(float amax, float& inverse) {

@@ -647,6 +647,9 @@ hipError_t run(DenseArgs a, int num_cus, hipStream_t st) {
   const int tn = D::GATED ? D::TN / 2 : D::TN;
   a.n_nt = (a.N + tn - 1) / tn;
   a.n_tt = (int)((a.T + D::TT - 1) / D::TT);
+  // a launch holds fewer than 2^32 threads: tiles that are not persistent are
+  // chosen for few tiles, or for N <= 64 with K >= 1920, of which memory holds
+  // fewer than 2^22
   const int items = a.n_nt * a.n_tt, grid = D::kPersistent ? std::min(items, num_cus) : items;
   hipLaunchKernelGGL((k_dense_fp8<FA, FB, WN, WT, MODE, STAGES, NP>), dim3((unsigned)grid), dim3(D::kThreads), 0, st,
                      a);

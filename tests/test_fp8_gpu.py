@@ -195,6 +195,52 @@ def test_dense_writes_only_its_rows(T):
     assert ((b[2:].float() - y[1:T + 1]).abs() <= y[1:T + 1].abs() * 2.0 ** -8 + 1e-2 * y[1:T + 1].square().mean().sqrt()).all()
 
 
+def _big(shape, seed, kind):
+    """Codes below NaN, or scales, made on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if kind == "codes":
+        return torch.randint(0, 0x7E, shape, dtype=torch.uint8, device="cuda", generator=g).view(F8)
+    return torch.rand(shape, device="cuda", generator=g) * 0.01
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("T,N,K", [((1 << 20) + 77, 64, 4112), (140003, 32772, 16)])
+def test_dense_offsets_beyond_32_bits(T, N, K, f32):
+    """Rows and outputs past 2^32 elements: the last rows equal those of a call
+    of their own (a row's sums have one order in every kernel of a mode)."""
+    x, xs = _big((T, K), 1, "codes"), _big((T, fp8.blocks(K)), 2, "scales")
+    w, ws = _big((N, K), 3, "codes"), _big((fp8.blocks(N), fp8.blocks(K)), 4, "scales")
+    y = torch.full((T, N), float("nan"), dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+    at = T // 4 * 4 - 200
+    part = torch.empty(T - at, N, dtype=y.dtype, device="cuda")
+    lm.dense_fp8(x, xs, w, ws, **{"y_f32" if f32 else "y_bf16": y})
+    lm.dense_fp8(x[at:], xs[at:], w, ws, **{"y_f32" if f32 else "y_bf16": part})
+    torch.cuda.synchronize()
+    assert torch.equal(y[at:], part) and torch.isfinite(part).all()
+
+
+def test_ffn_offsets_beyond_32_bits():
+    T, C, F = 140003, 16, 32768
+    x, xs = _big((T, C), 1, "codes"), _big((T, 1), 2, "scales")
+    gu, gus = _big((2 * F, C), 3, "codes"), _big((2, F // 128, 1), 4, "scales")
+    d, ds = _big((C, F), 5, "codes"), _big((1, F // 128), 6, "scales")
+    at = T // 4 * 4 - 200
+    out = []
+    for first in (0, at):
+        y = torch.full((T - first, C), float("nan"), dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(lm.ffn_fp8_workspace_size(T - first, C, F), dtype=torch.uint8, device="cuda")
+        lm.ffn_fp8(x[first:], xs[first:], gu, gus, d, ds, ws, y_bf16=y)
+        torch.cuda.synchronize()
+        out.append(y[at - first:].clone())
+    assert torch.equal(out[0], out[1]) and torch.isfinite(out[0]).all()
+
+
+def test_ffn_workspace_for_many_tokens_holds_fewer():
+    for C, F in ((64, 16), (4096, 2048), (1024, 65536)):
+        sizes = [lm.ffn_fp8_workspace_size(T, C, F) for T in (1, 8, 16, 17, 33, 64, 511, 512, 513, 4096, 70000)]
+        assert sizes == sorted(sizes)
+
+
 def _ffn_inputs(rng, T, C, F):
     x, xs = _x(rng, T, C)
     g, gs = _w(rng, F, C)

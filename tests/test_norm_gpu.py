@@ -219,3 +219,34 @@ def test_norm_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(o["r"], ref["r"]) and torch.equal(o["s"], ref["s"])
         assert torch.equal(o["c"].view(torch.uint8), ref["c"].view(torch.uint8))
+
+
+@pytest.mark.parametrize("what,rows", [("norm", (1 << 26) + 3), ("quantize", (1 << 28) + 5)])
+def test_more_threads_than_one_grid_dimension_holds(what, rows):
+    """2^32 threads and more, and elements past 2^32: short rows, of which a
+    pattern of 1024 repeats."""
+    C, n = 16, 1024
+    base = _rows(np.random.default_rng(31), n, C, BF16)
+    w = torch.from_numpy(np.random.default_rng(32).standard_normal(C).astype(np.float32)).cuda()
+
+    def run(x):
+        codes = torch.full(x.shape, 0x55, dtype=torch.uint8, device="cuda").view(F8)
+        scales = torch.full((x.shape[0], 1), float("nan"), device="cuda")
+        if what == "norm":
+            lm.rmsnorm(x, w, 1e-5, y_fp8=codes, y_scales=scales)
+        else:
+            lm.quantize_fp8(x, codes, scales)
+        torch.cuda.synchronize()
+        return codes.view(torch.uint8), scales
+
+    x = torch.empty(rows, C, dtype=BF16, device="cuda")
+    whole = rows // n * n
+    x[:whole].view(-1, n, C).copy_(base.expand(whole // n, n, C))
+    x[whole:] = base[:rows - whole]
+    codes, scales = run(x)
+    del x
+    c, s = run(base)
+    for at in range(0, whole, n << 16):
+        end = min(whole, at + (n << 16))
+        assert (codes[at:end].view(-1, n, C) == c).all() and (scales[at:end].view(-1, n, 1) == s).all()
+    assert torch.equal(codes[whole:], c[:rows - whole]) and torch.equal(scales[whole:], s[:rows - whole])
