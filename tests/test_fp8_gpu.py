@@ -161,6 +161,55 @@ def test_dense_rounded_outputs_alone(T, N, K):
         assert (np.abs(v.reshape(T, N) - full) <= step * (0.5 + 127 * 2.0 ** -11 + 1e-3) + np.abs(full) * 2.0 ** -8).all()
 
 
+@pytest.mark.parametrize("T,N,K", [(T, N, K) for T in (1, 20, 70) for N, K in ((1 << 20, 16), (72, 65536))])
+def test_dense_largest_weights(T, N, K):
+    rng = np.random.default_rng(T + K)
+    (x, xs), (w, ws) = _x(rng, T, K), _w(rng, N, K)
+    d = tuple(_dev(a) for a in (x, xs, w, ws))
+    y, b, _ = _dense(*d)
+    ref, mag = fp8.dense(x, xs, w, ws)
+    tol = _tol(ref, mag, K)
+    assert (np.abs(y.cpu().numpy() - ref) <= tol).all() and torch.equal(b, y.to(torch.bfloat16))
+    b = _dense(*d, f32=False)[1].double().cpu().numpy()
+    n = slice(N - 5000 if N > 5000 else 0, N)
+    if T > 16:
+        # blocks of scales of their own: the cut of the rows that are compared
+        first = n.start // 128 * 128
+        tol[:, n] += _cut(x, xs, w[first:], ws[first // 128:])[:, n.start - first:]
+    assert (np.abs(b - ref)[:, n] <= (tol * (1 + 2.0 ** -8) + np.abs(ref) * 2.0 ** -8)[:, n]).all()
+
+
+def test_calls_at_once_on_two_streams():
+    """Two gated blocks and two projections in flight together, each with its
+    own workspace, give what they give alone."""
+    rng = np.random.default_rng(77)
+    cases, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for T, C, F in ((700, 656, 1040), (6, 1024, 512)):
+        args = tuple(_dev(a) for a in _ffn_inputs(rng, T, C, F))
+        ws = torch.empty(lm.ffn_fp8_workspace_size(T, C, F), dtype=torch.uint8, device="cuda")
+        ys = [torch.empty(T, C, dtype=torch.bfloat16, device="cuda") for _ in range(9)]
+        ds = [torch.empty(T, 2 * F, device="cuda") for _ in range(9)]
+        cases.append((args, ws, ys, ds))
+
+    def run(case, i):
+        (x, xs, gu, gus, d, dsc), ws, ys, ds = case
+        lm.ffn_fp8(x, xs, gu, gus, d, dsc, ws, y_bf16=ys[i])
+        if gus.shape[1] * 128 == gu.shape[0] // 2:  # whole blocks: gate and up rows are one matrix
+            lm.dense_fp8(x, xs, gu, gus.view(-1, gus.shape[2]), y_f32=ds[i])
+
+    for case in cases:
+        run(case, 0)
+    torch.cuda.synchronize()
+    for i in range(1, 9):
+        for case, stream in zip(cases, streams):
+            with torch.cuda.stream(stream):
+                run(case, i)
+    torch.cuda.synchronize()
+    for (_, _, ys, ds), whole in zip(cases, (False, True)):
+        assert all(torch.equal(ys[0], y) for y in ys[1:])
+        assert not whole or all(torch.equal(ds[0], y) for y in ds[1:])
+
+
 @pytest.mark.parametrize("T", [5, 70, 2200])
 def test_dense_nan_codes_reach_their_outputs_only(T):
     """NaN codes stand where a wrong address would read: the row after the last
@@ -268,7 +317,8 @@ def _ffn(args, T, C, F, h=True, f32=True):
                                    for C, F in ((16, 16), (128, 128), (400, 272), (1024, 512), (256, 1040), (2064, 144))]
                          + [(8, 128, 2064), (9, 128, 272), (700, 2064, 1040), (530, 2064, 1936), (700, 656, 272),
                             (700, 272, 1040), (700, 272, 4112), (2100, 400, 2064), (5200, 144, 272),
-                            (9000, 144, 528), (6000, 144, 528), (2500, 656, 2576)])
+                            (9000, 144, 528), (6000, 144, 528), (2500, 656, 2576),
+                            (4, 65536, 16), (70, 65536, 16), (4, 16, 65536), (70, 16, 65536)])
 def test_ffn_matches_oracle_stage_by_stage(T, C, F):
     rng = np.random.default_rng(T + C + F)
     args = _ffn_inputs(rng, T, C, F)
@@ -284,8 +334,11 @@ def test_ffn_matches_oracle_stage_by_stage(T, C, F):
         G, U, H = G[t], U[t], H[t]
     else:
         t = slice(0, T)
-    # |d silu| <= 1.1 |dG|; exp, the division and the product in fp32: 8 roundings
-    dH = 1.1 * dG * (np.abs(U) + dU) + np.abs(H / np.where(U == 0, 1, U)) * dU + np.abs(H) * 8 * 2.0 ** -24
+    # |d silu| <= 1.1 |dG|; exp, the division and the product in fp32: 8 roundings.
+    # d(silu(G) U) = dsilu (U + dU) + silu(G) dU: the last factor is silu itself and
+    # not H / U, which says nothing where the products of U cancel to exactly 0
+    # (the matrix unit's cut leaves up to dU there)
+    dH = 1.1 * dG * (np.abs(U) + dU) + np.abs(fp8.silu_product(G, 1.0)) * dU + np.abs(H) * 8 * 2.0 ** -24
     hcn, hsn = hc.view(torch.uint8).cpu().numpy(), hs.cpu().numpy()
     hct, hst = hcn[t], hsn[t]
     pad = lambda a: np.pad(a, ((0, 0), (0, -F % 128))).reshape(len(a), -1, 128)
