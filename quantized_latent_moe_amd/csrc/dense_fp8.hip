@@ -36,8 +36,9 @@
 // What bounds it: direct loads reach about 100 GB/s a CU, 0.48 us for a step
 // of 256 x 128, and the MFMAs of that step take 0.5 to 0.57 us (the clock
 // falls to 1.8 GHz under them); together, with the LDS reads between, 0.86 us.  A
-// small tile's step is a chain (barrier, LDS reads, MFMAs, barrier): 0.20 us
-// for 64 x 64 on one CU, whatever the number of stages.  21000 x 4096 rows by
+// small tile's step is its loads: 0.20 us for the 16 KB of 64 x 64 on one CU,
+// and 8 stages instead of 4, a barrier for two steps or a second set of
+// fragment registers leave it there.  21000 x 4096 rows by
 // 4096 weights take 347 us (2030 TF; as much through the bf16 MFMA with an fp32
 // y 640 us, 1100 TF).
 #include <algorithm>
