@@ -218,7 +218,7 @@ bool fp8_dense_ok(int64_t T, int32_t N, int32_t K) {
 }
 hipError_t dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int64_t T, int N, int K,
                      float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus, hipStream_t st) {
-  if (T <= (y_f32 ? kFp8SmallExactT : kFp8SmallT))
+  if (T <= kFp8SmallT || (y_f32 && fp8_small_exact(T, N, num_cus)))
     return launch_dense_fp8_small(x, xs, w, ws, (int)T, N, K, y_f32, y_bf16, y_q8, st);
   return launch_dense_fp8(x, xs, w, ws, T, N, K, y_f32, y_bf16, y_q8, num_cus, st);
 }

@@ -1,5 +1,6 @@
-// Products of e4m3 rows with e4m3 weights for few tokens (decode): the formulas
-// of the tile kernel, arranged to stream the weights.
+// Products of e4m3 rows with e4m3 weights for few tokens (decode), and exact
+// ones for few weight rows: the formulas of the tile kernel, arranged to stream
+// the weights.
 //
 // Each weight is used for a few tokens only, so the time is that of reading
 // the weights once, and the products are exact: codes are widened to bf16 for
@@ -19,7 +20,12 @@
 //   4096 x 4096:  7.0 | 7.8 .. 9.6, bf16 tiles 8.7, fp32 (exact) tiles 13.4
 //   8192 x 2048:  6.7 | 7.3 .. 9.4, bf16 tiles 6.0, fp32 (exact) tiles 8.4
 // so a call for rounded outputs comes here up to 16 tokens, one for the fp32 y
-// up to 32 (beyond, a fragment of 16 tokens more costs 3 us and more).
+// up to 32.  Larger batches come in groups of 32 tokens, one a workgroup; with a
+// CU for each workgroup that beats the exact tiles, whose step of K is as long
+// on one CU as on all (us here | tiles):
+//   64 tokens, 1024 x 4096:  9.1 | 13.5, 128 tokens  9.6 | 13.8 (256 workgroups)
+//   512 tokens, 256 x 8192: 17.3 | 24.4, 33 tokens, 2048 x 2048  5.7 | 8.2
+// and with two on a CU it does not: 256 tokens, 1024 x 4096  16.5 | 13.8.
 #include "block_fp8.h"
 
 namespace latmoe {
@@ -63,7 +69,7 @@ enum SmallMode : int { kRows = 0, kGatedPair = 1, kRound = 2 };
 constexpr int small_waves(int tf) { return tf == 1 ? 16 : 8; }
 
 template <int FR, int TF, int MODE>
-__global__ __launch_bounds__(64 * small_waves(TF)) void k_dense_fp8_small(const SmallArgs a) {
+__global__ __launch_bounds__(64 * small_waves(TF)) void k_dense_fp8_small(SmallArgs a) {
   constexpr bool GATED = MODE == kGatedPair;
   constexpr int kWaves = small_waves(TF), U = TF;  // U blocks in flight per wave
   constexpr int NF = GATED ? 8 : 16 * FR;              // output columns
@@ -75,6 +81,15 @@ __global__ __launch_bounds__(64 * small_waves(TF)) void k_dense_fp8_small(const 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int n0 = (int)blockIdx.x * NF;
+  if (TF == 2) {  // the workgroup's 32 tokens
+    const int64_t t0 = (int64_t)blockIdx.y * 32;
+    a.x += t0 * a.K;
+    a.xs += t0 * a.nb;
+    a.T = min(a.T - (int)t0, 32);
+    if (a.y_f32) a.y_f32 += t0 * a.N;
+    if (a.y_bf16) a.y_bf16 += t0 * a.N;
+    if (a.y_q8) a.y_q8 += t0 * (a.N / 32) * kQ81Bytes;
+  }
   const int K = a.K, nb = a.nb;
   const int nbn = (a.N + kFp8Block - 1) / kFp8Block;
 
@@ -228,7 +243,8 @@ void run(const SmallArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)((a.N + nf - 1) / nf));
   if constexpr (MODE == kRows) {
     if (a.T > 16) {
-      hipLaunchKernelGGL((k_dense_fp8_small<FR, 2, MODE>), grid, dim3(64 * small_waves(2)), 0, st, a);
+      const dim3 grid2(grid.x, (unsigned)((a.T + 31) / 32));
+      hipLaunchKernelGGL((k_dense_fp8_small<FR, 2, MODE>), grid2, dim3(64 * small_waves(2)), 0, st, a);
       return;
     }
   }

@@ -255,9 +255,13 @@ hipError_t launch_rmsnorm(const NormArgs& a, int num_cus, hipStream_t st);
 // e4m3 rows [T][K] x e4m3 weights [N][K] -> y in fp32, bf16 and/or q8_1 (any may be null, not all).
 hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int64_t T, int N,
                             int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus, hipStream_t st);
-// The same for at most kFp8SmallT tokens (kFp8SmallExactT where the fp32 y is
-// asked for), by a kernel that streams the weights.
-constexpr int kFp8SmallT = 16, kFp8SmallExactT = 32;
+// The same for at most kFp8SmallT tokens, by a kernel that streams the weights;
+// where the fp32 y is asked for, also for one group of 32 tokens, or for so few
+// weight rows and groups that each 16 rows and each group have a CU.
+constexpr int kFp8SmallT = 16;
+inline bool fp8_small_exact(int64_t T, int N, int num_cus) {
+  return T <= 32 || ((int64_t)N + 15) / 16 * ((T + 31) / 32) <= num_cus;
+}
 hipError_t launch_dense_fp8_small(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int T, int N,
                                   int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, hipStream_t st);
 // fp32 rows h [T][K] of at most kFp8RoundT tokens, rounded to e4m3 rows on the way, x e4m3 weights.

@@ -85,7 +85,8 @@ def _dense(x, xs, w, ws, f32=True, bf16=True, q8=False):
     return y, b, q
 
 
-# every kernel: few tokens (one and two token fragments), tiles; each with
+# every kernel: few tokens (one and two token fragments, groups of 32 tokens for
+# few weight rows), tiles; each with
 # whole and ragged N and K, and K of an odd and an even number of blocks
 @pytest.mark.parametrize("N,K", [(1, 16), (16, 128), (31, 144), (64, 1024), (130, 400), (260, 2064), (1024, 4096),
                                  (4100, 272), (515, 640)])
@@ -229,7 +230,7 @@ def test_dense_nan_codes_reach_their_outputs_only(T):
     assert torch.equal(y2[keep], y[keep])
 
 
-@pytest.mark.parametrize("T", [4, 200])
+@pytest.mark.parametrize("T", [4, 200, 1100])
 def test_dense_writes_only_its_rows(T):
     rng = np.random.default_rng(4)
     N, K = 132, 256
@@ -256,11 +257,12 @@ def _big(shape, seed, kind):
 @pytest.mark.parametrize("T,N,K", [((1 << 20) + 77, 64, 4112), (140003, 32772, 16)])
 def test_dense_offsets_beyond_32_bits(T, N, K, f32):
     """Rows and outputs past 2^32 elements: the last rows equal those of a call
-    of their own (a row's sums have one order in every kernel of a mode)."""
+    of their own, large enough for tiles too (a row's sums have one order in
+    every tile kernel of a mode)."""
     x, xs = _big((T, K), 1, "codes"), _big((T, fp8.blocks(K)), 2, "scales")
     w, ws = _big((N, K), 3, "codes"), _big((fp8.blocks(N), fp8.blocks(K)), 4, "scales")
     y = torch.full((T, N), float("nan"), dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
-    at = T // 4 * 4 - 200
+    at = T // 4 * 4 - 10000
     part = torch.empty(T - at, N, dtype=y.dtype, device="cuda")
     lm.dense_fp8(x, xs, w, ws, **{"y_f32" if f32 else "y_bf16": y})
     lm.dense_fp8(x[at:], xs[at:], w, ws, **{"y_f32" if f32 else "y_bf16": part})
