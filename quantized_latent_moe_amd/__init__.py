@@ -38,8 +38,10 @@ EXPORTED = (
     "lat_moe_quantize_fp8",
     "lat_moe_rmsnorm",
     "lat_moe_dense_fp8",
+    "lat_moe_dense_fp8_ex",
     "lat_moe_ffn_fp8_workspace_size",
     "lat_moe_ffn_fp8",
+    "lat_moe_ffn_fp8_ex",
     "lat_moe_strerror",
     "lat_moe_version",
 )
@@ -116,10 +118,14 @@ def lib() -> ctypes.CDLL:
         c.lat_moe_rmsnorm.restype = ctypes.c_int
         c.lat_moe_dense_fp8.argtypes = [P, P, P, P, i64, i32, i32, P, P, P, P]
         c.lat_moe_dense_fp8.restype = ctypes.c_int
+        c.lat_moe_dense_fp8_ex.argtypes = [P, P, P, P, i64, i32, i32, P, P, P, i32, P]
+        c.lat_moe_dense_fp8_ex.restype = ctypes.c_int
         c.lat_moe_ffn_fp8_workspace_size.argtypes = [i64, i32, i32]
         c.lat_moe_ffn_fp8_workspace_size.restype = size
         c.lat_moe_ffn_fp8.argtypes = [P, P, P, P, P, P, i64, i32, i32, P, P, P, P, P, size, P]
         c.lat_moe_ffn_fp8.restype = ctypes.c_int
+        c.lat_moe_ffn_fp8_ex.argtypes = [P, P, P, P, P, P, i64, i32, i32, P, P, P, P, i32, P, size, P]
+        c.lat_moe_ffn_fp8_ex.restype = ctypes.c_int
         c.lat_moe_strerror.argtypes = [ctypes.c_int]
         c.lat_moe_strerror.restype = ctypes.c_char_p
         c.lat_moe_version.restype = ctypes.c_int
@@ -370,11 +376,26 @@ def _matrix(name: str, codes, scales, lead, N: int, K: int, e4m3, f32, dev):
             _tensor(name + "'s scales", scales, f32, (lead, *blocks) if lead else blocks, dev))
 
 
-def dense_fp8(x_fp8, x_scales, w_fp8, w_scales, *, y_f32=None, y_bf16=None, y_q8_1=None, stream=None) -> None:
+def _products(exact) -> int:
+    """How products with more than 16 rows are computed.  None: exactly where
+    an fp32 y is asked for (the gated block's gate and up products never);
+    True: exactly; False: by the e4m3 matrix unit."""
+    if exact is None:
+        return 0
+    if exact is not True and exact is not False:
+        raise ValueError(f"exact has to be True, False or None, got {exact!r}")
+    return 1 if exact else 2
+
+
+def dense_fp8(x_fp8, x_scales, w_fp8, w_scales, *, y_f32=None, y_bf16=None, y_q8_1=None, exact=None,
+              stream=None) -> None:
     """Projection of e4m3 rows x_fp8 (float8_e4m3fn [T, K]) with x_scales
     (float32 [T, ceil(K/128)]) by e4m3 weights w_fp8 (float8_e4m3fn [N, K])
     with w_scales (float32 [ceil(N/128), ceil(K/128)]) -> y_f32 (float32
-    [T, N]), y_bf16 (bfloat16 [T, N]) and/or y_q8_1 (uint8 [T, N/32, 36])."""
+    [T, N]), y_bf16 (bfloat16 [T, N]) and/or y_q8_1 (uint8 [T, N/32, 36]).
+    With more than 16 rows the products are exact if y_f32 is given, and pass
+    through the e4m3 matrix unit, which cuts small ones beside large ones,
+    otherwise (about twice as fast); exact=True or False chooses."""
     e4m3, f32, bf16, u8, _, cur, raw = _torch()
     if x_fp8.dim() != 2 or w_fp8.dim() != 2:
         raise ValueError("x_fp8 and w_fp8 have to be 2-dimensional")
@@ -382,12 +403,12 @@ def dense_fp8(x_fp8, x_scales, w_fp8, w_scales, *, y_f32=None, y_bf16=None, y_q8
     N = w_fp8.shape[0]
     dev = _device("x_fp8", x_fp8, cur)
     w, ws = _matrix("w_fp8", w_fp8, w_scales, 0, N, K, e4m3, f32, dev)
-    rc = lib().lat_moe_dense_fp8(_tensor("x_fp8", x_fp8, e4m3, shape, dev),
-                                 _tensor("x_scales", x_scales, f32, (T, -(-K // 128)), dev), w, ws, T, N, K,
-                                 None if y_f32 is None else _tensor("y_f32", y_f32, f32, (T, N), dev),
-                                 None if y_bf16 is None else _tensor("y_bf16", y_bf16, bf16, (T, N), dev),
-                                 None if y_q8_1 is None else _tensor("y_q8_1", y_q8_1, u8, (T, N // 32, 36), dev),
-                                 raw(dev) if stream is None else int(stream))
+    rc = lib().lat_moe_dense_fp8_ex(_tensor("x_fp8", x_fp8, e4m3, shape, dev),
+                                    _tensor("x_scales", x_scales, f32, (T, -(-K // 128)), dev), w, ws, T, N, K,
+                                    None if y_f32 is None else _tensor("y_f32", y_f32, f32, (T, N), dev),
+                                    None if y_bf16 is None else _tensor("y_bf16", y_bf16, bf16, (T, N), dev),
+                                    None if y_q8_1 is None else _tensor("y_q8_1", y_q8_1, u8, (T, N // 32, 36), dev),
+                                    _products(exact), raw(dev) if stream is None else int(stream))
     if rc:
         _check(rc)
 
@@ -400,14 +421,18 @@ def ffn_fp8_workspace_size(T: int, C: int, F: int) -> int:
 
 
 def ffn_fp8(x_fp8, x_scales, gateup_fp8, gateup_scales, down_fp8, down_scales, workspace, *, y_f32=None, y_bf16=None,
-            h_fp8=None, h_scales=None, stream=None) -> None:
+            h_fp8=None, h_scales=None, exact=None, stream=None) -> None:
     """Gated feed-forward block on e4m3 rows x_fp8 [T, C] (x_scales [T,
     ceil(C/128)]): silu(x gate^T) * (x up^T), rounded to e4m3 rows, times
     down^T.  gateup_fp8 is [2F, C], the gate rows first, with gateup_scales
     [2, ceil(F/128), ceil(C/128)]; down_fp8 [C, F] with down_scales
     [ceil(C/128), ceil(F/128)]; y_f32 and/or y_bf16 are [T, C]; h_fp8 [T, F]
     and h_scales [T, ceil(F/128)] take H if they are given; workspace is a
-    uint8 tensor of at least ffn_fp8_workspace_size(T, C, F) bytes."""
+    uint8 tensor of at least ffn_fp8_workspace_size(T, C, F) bytes.  With more
+    than 16 rows the gate and up products pass through the e4m3 matrix unit, so
+    that 0.24% of H's codes differ from those of exact products, and the down
+    products are exact if y_f32 is given; exact=True makes all exact, False
+    none."""
     e4m3, f32, bf16, u8, _, cur, raw = _torch()
     if x_fp8.dim() != 2 or down_fp8.dim() != 2:
         raise ValueError("x_fp8 and down_fp8 have to be 2-dimensional")
@@ -417,15 +442,15 @@ def ffn_fp8(x_fp8, x_scales, gateup_fp8, gateup_scales, down_fp8, down_scales, w
     gu, gus = _matrix("gateup_fp8", gateup_fp8, gateup_scales, 2, F, C, e4m3, f32, dev)
     dn, dns = _matrix("down_fp8", down_fp8, down_scales, 0, C, F, e4m3, f32, dev)
     nbytes = workspace.numel()
-    rc = lib().lat_moe_ffn_fp8(_tensor("x_fp8", x_fp8, e4m3, shape, dev),
-                               _tensor("x_scales", x_scales, f32, (T, -(-C // 128)), dev), gu, gus, dn, dns, T, C, F,
-                               None if y_f32 is None else _tensor("y_f32", y_f32, f32, shape, dev),
-                               None if y_bf16 is None else _tensor("y_bf16", y_bf16, bf16, shape, dev),
-                               None if h_fp8 is None else _tensor("h_fp8", h_fp8, e4m3, (T, F), dev),
-                               None if h_scales is None else _tensor("h_scales", h_scales, f32, (T, -(-F // 128)),
-                                                                     dev),
-                               _tensor("workspace", workspace, u8, (nbytes,), dev), nbytes,
-                               raw(dev) if stream is None else int(stream))
+    rc = lib().lat_moe_ffn_fp8_ex(_tensor("x_fp8", x_fp8, e4m3, shape, dev),
+                                  _tensor("x_scales", x_scales, f32, (T, -(-C // 128)), dev), gu, gus, dn, dns, T, C, F,
+                                  None if y_f32 is None else _tensor("y_f32", y_f32, f32, shape, dev),
+                                  None if y_bf16 is None else _tensor("y_bf16", y_bf16, bf16, shape, dev),
+                                  None if h_fp8 is None else _tensor("h_fp8", h_fp8, e4m3, (T, F), dev),
+                                  None if h_scales is None else _tensor("h_scales", h_scales, f32, (T, -(-F // 128)),
+                                                                        dev),
+                                  _products(exact), _tensor("workspace", workspace, u8, (nbytes,), dev), nbytes,
+                                  raw(dev) if stream is None else int(stream))
     if rc:
         _check(rc)
 

@@ -217,10 +217,17 @@ bool fp8_dense_ok(int64_t T, int32_t N, int32_t K) {
   return ((T + 63) / 64) * (((int64_t)N + 63) / 64) < (int64_t)1 << 31;
 }
 hipError_t dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int64_t T, int N, int K,
-                     float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus, hipStream_t st) {
-  if (T <= kFp8SmallT || (y_f32 && fp8_small_exact(T, N, num_cus)))
+                     bool exact, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus, hipStream_t st) {
+  if (T <= kFp8SmallT || (exact && fp8_small_exact(T, N, num_cus)))
     return launch_dense_fp8_small(x, xs, w, ws, (int)T, N, K, y_f32, y_bf16, y_q8, st);
-  return launch_dense_fp8(x, xs, w, ws, T, N, K, y_f32, y_bf16, y_q8, num_cus, st);
+  return launch_dense_fp8(x, xs, w, ws, T, N, K, exact, y_f32, y_bf16, y_q8, num_cus, st);
+}
+bool products_ok(int32_t products) {
+  return products == LAT_MOE_PRODUCTS_AUTO || products == LAT_MOE_PRODUCTS_EXACT || products == LAT_MOE_PRODUCTS_E4M3;
+}
+// Whether a projection to these outputs takes exact products.
+bool products_exact(int32_t products, const float* y_f32) {
+  return products == LAT_MOE_PRODUCTS_EXACT || (products == LAT_MOE_PRODUCTS_AUTO && y_f32);
 }
 
 bool ffn_fp8_ok(int64_t T, int32_t C, int32_t F) {
@@ -381,7 +388,14 @@ int lat_moe_rmsnorm(const void* x, int32_t x_type, const void* residual, int32_t
 
 int lat_moe_dense_fp8(const void* x_fp8, const float* x_scales, const void* w_fp8, const float* w_scales, int64_t T,
                       int32_t N, int32_t K, float* y_f32, void* y_bf16, void* y_q8_1, void* stream) {
-  if (!fp8_dense_ok(T, N, K)) return LAT_MOE_EINVAL;
+  return lat_moe_dense_fp8_ex(x_fp8, x_scales, w_fp8, w_scales, T, N, K, y_f32, y_bf16, y_q8_1, LAT_MOE_PRODUCTS_AUTO,
+                              stream);
+}
+
+int lat_moe_dense_fp8_ex(const void* x_fp8, const float* x_scales, const void* w_fp8, const float* w_scales, int64_t T,
+                         int32_t N, int32_t K, float* y_f32, void* y_bf16, void* y_q8_1, int32_t products,
+                         void* stream) {
+  if (!fp8_dense_ok(T, N, K) || !products_ok(products)) return LAT_MOE_EINVAL;
   if (y_q8_1 && N % 32) return LAT_MOE_EINVAL;
   if (T == 0) return LAT_MOE_OK;
   if (!y_f32 && !y_bf16 && !y_q8_1) return LAT_MOE_EINVAL;
@@ -393,8 +407,8 @@ int lat_moe_dense_fp8(const void* x_fp8, const float* x_scales, const void* w_fp
   int rc = check_device(&num_cus);
   if (rc != LAT_MOE_OK) return rc;
   if (dense_fp8(static_cast<const uint8_t*>(x_fp8), x_scales, static_cast<const uint8_t*>(w_fp8), w_scales, T, N, K,
-                y_f32, static_cast<uint16_t*>(y_bf16), static_cast<uint8_t*>(y_q8_1), num_cus,
-                static_cast<hipStream_t>(stream)) != hipSuccess)
+                products_exact(products, y_f32), y_f32, static_cast<uint16_t*>(y_bf16), static_cast<uint8_t*>(y_q8_1),
+                num_cus, static_cast<hipStream_t>(stream)) != hipSuccess)
     return LAT_MOE_ELAUNCH;
   return LAT_MOE_OK;
 }
@@ -407,7 +421,15 @@ int lat_moe_ffn_fp8(const void* x_fp8, const float* x_scales, const void* gateup
                     const void* down_fp8, const float* down_scales, int64_t T, int32_t C, int32_t F, float* y_f32,
                     void* y_bf16, void* h_fp8, float* h_scales, void* workspace, size_t workspace_bytes,
                     void* stream) {
-  if (!ffn_fp8_ok(T, C, F)) return LAT_MOE_EINVAL;
+  return lat_moe_ffn_fp8_ex(x_fp8, x_scales, gateup_fp8, gateup_scales, down_fp8, down_scales, T, C, F, y_f32, y_bf16,
+                            h_fp8, h_scales, LAT_MOE_PRODUCTS_AUTO, workspace, workspace_bytes, stream);
+}
+
+int lat_moe_ffn_fp8_ex(const void* x_fp8, const float* x_scales, const void* gateup_fp8, const float* gateup_scales,
+                       const void* down_fp8, const float* down_scales, int64_t T, int32_t C, int32_t F, float* y_f32,
+                       void* y_bf16, void* h_fp8, float* h_scales, int32_t products, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (!ffn_fp8_ok(T, C, F) || !products_ok(products)) return LAT_MOE_EINVAL;
   if (T == 0) return LAT_MOE_OK;
   if (!y_f32 && !y_bf16) return LAT_MOE_EINVAL;
   if ((h_fp8 == nullptr) != (h_scales == nullptr)) return LAT_MOE_EINVAL;
@@ -441,11 +463,13 @@ int lat_moe_ffn_fp8(const void* x_fp8, const float* x_scales, const void* gateup
                  ? LAT_MOE_OK
                  : LAT_MOE_ELAUNCH;
     if (launch_quantize_fp8(h32, LAT_MOE_F32, T, F, h, hs, st) != hipSuccess) return LAT_MOE_ELAUNCH;
-  } else if (launch_gateup_fp8(x, x_scales, gu, gateup_scales, T, F, C, h32, h, hs, num_cus, st) != hipSuccess) {
+  } else if (launch_gateup_fp8(x, x_scales, gu, gateup_scales, T, F, C, products == LAT_MOE_PRODUCTS_EXACT, h32,
+                               h, hs, num_cus, st) != hipSuccess) {
     return LAT_MOE_ELAUNCH;
   }
-  if (dense_fp8(h, hs, static_cast<const uint8_t*>(down_fp8), down_scales, T, C, F, y_f32,
-                static_cast<uint16_t*>(y_bf16), nullptr, num_cus, st) != hipSuccess)
+  if (dense_fp8(h, hs, static_cast<const uint8_t*>(down_fp8), down_scales, T, C, F,
+                products_exact(products, y_f32), y_f32, static_cast<uint16_t*>(y_bf16), nullptr, num_cus,
+                st) != hipSuccess)
     return LAT_MOE_ELAUNCH;
   return LAT_MOE_OK;
 }
@@ -462,6 +486,6 @@ const char* lat_moe_strerror(int code) {
   }
 }
 
-int lat_moe_version(void) { return 200; }
+int lat_moe_version(void) { return 201; }
 
 }  // extern "C"

@@ -13,11 +13,15 @@
 // (toward zero) to a multiple of 2^-13 of the power of two of the group's
 // largest exponent, and the groups in fp32 (found by feeding it pairs of
 // products of known size).  On Gaussian data that is 1.5e-5 of y's norm: 100
-// times below the rounding of a bf16 y (1.7e-3), and further below those of
-// q8_1 and e4m3, so these outputs take it.  A call that asks for the fp32 y
-// gets exact products instead: the codes are widened to bf16 in registers
-// (two a VALU operation), and four bf16 MFMAs a block (error 1e-8) take twice
-// the matrix time.
+// times below the rounding of a bf16 y (1.7e-3), so calls for rounded outputs
+// take it unless they ask for exact products.  It is more where large products
+// cancel and small ones beside them are what is left, and where a rounding to
+// few bits follows: in the gated block 0.24% of H's codes become their
+// neighbours, which are as near, and that moves y by 1.2e-3 of its norm (H's
+// rounding itself by 2.3e-2, with either products).  Exact products, which the fp32 y of a projection
+// takes unless the call says otherwise: the codes are widened to bf16 in
+// registers (two a VALU operation), and four bf16 MFMAs a block take twice the
+// matrix time.
 //
 // One workgroup computes TN = 16 FA WN weight rows x TT = 16 FB WT tokens.
 // Weights are the MFMA's row operand: a lane then holds four neighbouring
@@ -120,12 +124,16 @@ __device__ __forceinline__ void tile_of(const DenseArgs& a, int number, int& nt,
 
 // What a tile kernel computes: the projection with e4m3 products, the
 // projection with bf16 products, or the gated pair of projections with H
-// rounded to e4m3 (a tile then holds 128 columns of H, one scale's) or in fp32.
-enum Mode : int { kFast = 0, kExact = 1, kGated = 2, kGatedRaw = 3 };
+// rounded to e4m3 (a tile then holds 128 columns of H, one scale's) or in fp32,
+// each of them with e4m3 or (Exact) bf16 products.
+enum Mode : int { kFast = 0, kExact = 1, kGated = 2, kGatedRaw = 3, kGatedExact = 4, kGatedRawExact = 5 };
+constexpr bool is_exact(int mode) { return mode == kExact || mode == kGatedExact || mode == kGatedRawExact; }
+// H is rounded where it is made.
+constexpr bool is_rounded(int mode) { return mode == kGated || mode == kGatedExact; }
 
 template <int FA, int FB, int WN, int WT, int MODE, int STAGES, int NP>
 struct Tile {
-  static constexpr bool GATED = MODE == kGated || MODE == kGatedRaw;
+  static constexpr bool GATED = MODE >= kGated, EXACT = is_exact(MODE);
   static constexpr int kWaves = WN * WT;                // that multiply; NP more load
   static constexpr int kThreads = 64 * (kWaves + NP);
   static constexpr int TN = 16 * FA * WN, TT = 16 * FB * WT;
@@ -140,7 +148,7 @@ struct Tile {
   static_assert(TN % (8 * NP) == 0 && TT % (8 * NP) == 0, "whole loads");
   static_assert(TT % 64 == 0, "a load takes 64 tokens' scales");
   static_assert(STAGES >= 2, "at least a step ahead");
-  static_assert(MODE != kGated || TN == 256, "a gated tile holds one e4m3 block of H");
+  static_assert(!is_rounded(MODE) || TN == 256, "a gated tile holds one e4m3 block of H");
 
   // H column (within the tile) of LDS row r of the weight tile, gated tiles:
   // each wave's 16 FA rows are FA/2 gate fragments and the same columns' up
@@ -246,13 +254,13 @@ struct Tile {
     return v8i{l[0], l[1], l[2], l[3], h[0], h[1], h[2], h[3]};
   }
 
-  // An MFMA operand of 16 rows and K = 128: the e4m3 codes, or (kExact) the
+  // An MFMA operand of 16 rows and K = 128: the e4m3 codes, or (EXACT) the
   // same values in bf16 (e4m3 is a subset of bf16).
   struct Codes { v8i v; };
   struct Wide { v8bf v[4]; };
-  using Operand = std::conditional_t<MODE == kExact, Wide, Codes>;
+  using Operand = std::conditional_t<EXACT, Wide, Codes>;
   static __device__ __forceinline__ Operand operand(v8i f) {
-    if constexpr (MODE == kExact) {
+    if constexpr (EXACT) {
       Wide o;
 #pragma unroll
       for (int q = 0; q < 4; ++q) o.v[q] = widen(f[2 * q], f[2 * q + 1]);
@@ -263,7 +271,7 @@ struct Tile {
   }
   static __device__ __forceinline__ v4f product(const Operand& a, const Operand& b) {
     v4f p = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (MODE == kExact) {
+    if constexpr (EXACT) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[q], b.v[q], p, 0, 0, 0);
     } else {
@@ -278,7 +286,7 @@ struct Tile {
   // SIMD cover each other's waits and bf16 operands fill the registers, one is
   // enough; a wave alone (128 x 128 exact) takes 44 us with 1 and 37 with 3 for
   // 2048 x 2048 x 4096.
-  static constexpr int kLag = MODE == kExact && kWaves == 8 ? 1 : 3;
+  static constexpr int kLag = EXACT && kWaves == 8 ? 1 : 3;
   static constexpr int kSides = GATED ? 2 : 1;
   static_assert(FA * FB % (kLag + 1) == 0, "the results' registers come round with the step");
   struct State {
@@ -353,8 +361,8 @@ __global__ __launch_bounds__(64 * (WN * WT + NP)) void k_dense_fp8(const DenseAr
   constexpr bool GATED = D::GATED;
   __shared__ __align__(16) uint8_t As[STAGES * TN * kStep], Bs[STAGES * TT * kStep];
   __shared__ __align__(16) float sxs[kRunBuffers * TT * kScaleSteps];  // runs of [token][step]
-  constexpr int PARTS = MODE == kGated ? WN : 1;
-  __shared__ float part[PARTS][MODE == kGated ? TT : 1];  // largest |H| of a token in a wave's columns
+  constexpr int PARTS = is_rounded(MODE) ? WN : 1;
+  __shared__ float part[PARTS][is_rounded(MODE) ? TT : 1];  // largest |H| of a token in a wave's columns
 
   const int K = a.K, nb = a.nb;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -426,7 +434,7 @@ __global__ __launch_bounds__(64 * (WN * WT + NP)) void k_dense_fp8(const DenseAr
         if ((s & (kScaleSteps - 1)) == 0) load_next_run();
         load_next();
       }
-      if (MODE == kGated) lds_barrier();
+      if (is_rounded(MODE)) lds_barrier();
     }
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no load may still write LDS when the workgroup ends
     return;
@@ -487,7 +495,7 @@ __global__ __launch_bounds__(64 * (WN * WT + NP)) void k_dense_fp8(const DenseAr
     }
 
     const int r = lane & 15, g = lane >> 4;
-    if constexpr (MODE == kGatedRaw) {
+    if constexpr (MODE == kGatedRaw || MODE == kGatedRawExact) {
 #pragma unroll
       for (int j = 0; j < FB; ++j)
 #pragma unroll
@@ -680,11 +688,15 @@ constexpr Variant kGatedTiles[] = {{128, 128, 1, 4.f, 3.f, {0.86f}},
                                    // with the rounding in a launch of its own
                                    {64, 64, 2, 3.f, 4.f, {0.32f, 0.65f}},
                                    {32, 64, 2, 3.f, 3.f, {0.20f, 0.39f}}};
-// Variants that round H themselves.  128 columns of H are one scale's, so these
+// With exact products: H rounded, and fp32 H.  512 tokens of C = 4096, F = 2048
+// take 37.4 us for the whole block (27.5 with e4m3 products), 5268 with F = 8192
+// 913 us (553).
+constexpr Variant kGatedExactTiles[] = {{128, 64, 1, 4.f, 3.f, {0.95f}}, {32, 64, 2, 3.f, 4.f, {0.35f, 0.57f}}};
+// Variants that round H themselves come first, two and one.  128 columns of H are one scale's, so these
 // fill the chip only where T F is large: 65 tokens of C = 4096, F = 2048 (16
 // tiles of 128 x 64) took 24.0 us for the whole block, and take 16.9 us with
 // tiles of 32 columns, fp32 H and a launch that rounds it.
-constexpr int kGatedRounded = 2;
+constexpr int kGatedRounded = 2, kGatedExactRounded = 1;
 
 int pick(const Variant* v, int count, int64_t T, int N, int nb, int num_cus) {
   int best = 0;
@@ -705,9 +717,10 @@ int pick(const Variant* v, int count, int64_t T, int N, int nb, int num_cus) {
 }  // namespace
 
 hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int64_t T, int N,
-                            int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus, hipStream_t st) {
+                            int K, bool exact, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus,
+                            hipStream_t st) {
   const DenseArgs a{x, xs, w, ws, y_f32, y_bf16, y_q8, nullptr, nullptr, T, N, K, (K + kStep - 1) / kStep, 0, 0};
-  if (y_f32) {  // exact products (see the head of the file)
+  if (exact) {
     switch (pick(kExactTiles, 3, T, N, a.nb, num_cus)) {
       case 0: return run<4, 3, 2, 4, kExact, 3, 4>(a, num_cus, st);
       case 1: return run<4, 4, 2, 2, kExact, 3, 2>(a, num_cus, st);
@@ -723,14 +736,21 @@ hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w,
 }
 
 hipError_t launch_gateup_fp8(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int64_t T, int F,
-                             int C, float* h32, uint8_t* h, float* hs, int num_cus, hipStream_t st) {
+                             int C, bool exact, float* h32, uint8_t* h, float* hs, int num_cus, hipStream_t st) {
   const DenseArgs a{x, xs, gu, gus, h32, nullptr, nullptr, h, hs, T, F, C, (C + kStep - 1) / kStep, 0, 0};
-  const int choices = T * F <= kFp8H32 ? 4 : kGatedRounded;
-  const int variant = pick(kGatedTiles, choices, T, F, a.nb, num_cus);
-  if (variant == 0) return run<4, 4, 4, 2, kGated, 3, 4>(a, num_cus, st);
-  if (variant == 1) return run<8, 2, 2, 2, kGated, 3, 4>(a, num_cus, st);
-  const hipError_t e = variant == 2 ? run<4, 2, 2, 2, kGatedRaw, 3, 2>(a, num_cus, st)
-                                    : run<2, 2, 2, 2, kGatedRaw, 4, 4>(a, num_cus, st);
+  const bool raw = T * F <= kFp8H32;
+  hipError_t e;
+  if (exact) {
+    if (pick(kGatedExactTiles, raw ? 2 : kGatedExactRounded, T, F, a.nb, num_cus) < kGatedExactRounded)
+      return run<4, 2, 4, 2, kGatedExact, 3, 4>(a, num_cus, st);
+    e = run<2, 2, 2, 2, kGatedRawExact, 4, 4>(a, num_cus, st);
+  } else {
+    const int variant = pick(kGatedTiles, raw ? 4 : kGatedRounded, T, F, a.nb, num_cus);
+    if (variant == 0) return run<4, 4, 4, 2, kGated, 3, 4>(a, num_cus, st);
+    if (variant == 1) return run<8, 2, 2, 2, kGated, 3, 4>(a, num_cus, st);
+    e = variant == 2 ? run<4, 2, 2, 2, kGatedRaw, 3, 2>(a, num_cus, st)
+                     : run<2, 2, 2, 2, kGatedRaw, 4, 4>(a, num_cus, st);
+  }
   return e == hipSuccess ? launch_quantize_fp8(h32, LAT_MOE_F32, T, F, h, hs, st) : e;
 }
 

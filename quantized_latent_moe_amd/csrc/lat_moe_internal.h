@@ -253,10 +253,12 @@ struct NormArgs {
 };
 hipError_t launch_rmsnorm(const NormArgs& a, int num_cus, hipStream_t st);
 // e4m3 rows [T][K] x e4m3 weights [N][K] -> y in fp32, bf16 and/or q8_1 (any may be null, not all).
+// exact: products by the bf16 MFMA.
 hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int64_t T, int N,
-                            int K, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus, hipStream_t st);
-// The same for at most kFp8SmallT tokens, by a kernel that streams the weights;
-// where the fp32 y is asked for, also for one group of 32 tokens, or for so few
+                            int K, bool exact, float* y_f32, uint16_t* y_bf16, uint8_t* y_q8, int num_cus,
+                            hipStream_t st);
+// The same, exact, for at most kFp8SmallT tokens, by a kernel that streams the weights;
+// where exact products are asked for, also for one group of 32 tokens, or for so few
 // weight rows and groups that each 16 rows and each group have a CU.
 constexpr int kFp8SmallT = 16;
 inline bool fp8_small_exact(int64_t T, int N, int num_cus) {
@@ -277,6 +279,6 @@ hipError_t launch_gateup_fp8_small(const uint8_t* x, const float* xs, const uint
 // columns and 64 tokens are on half of the CUs and their rounding costs no launch.
 constexpr int64_t kFp8H32 = (int64_t)1 << 20;
 hipError_t launch_gateup_fp8(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int64_t T, int F,
-                             int C, float* h32, uint8_t* h, float* hs, int num_cus, hipStream_t st);
+                             int C, bool exact, float* h32, uint8_t* h, float* hs, int num_cus, hipStream_t st);
 
 }  // namespace latmoe
