@@ -336,7 +336,8 @@ int lat_moe_rmsnorm(const void* x, int32_t x_type, const void* residual, int32_t
  * At least one output must be given; all outputs of one call are made of the
  * same fp32 y.  Supported: T >= 0, T < 2^31, 1 <= N <= LAT_MOE_FP8_MAX_N, K % 16 == 0,
  * 16 <= K <= 65536, ceil(T/64) * ceil(N/64) < 2^31; pointers 16-byte aligned.
- * A code that is a NaN makes the outputs that it enters NaN and no others.
+ * A code that is a NaN makes the outputs that it enters NaN and no others; a
+ * q8_1 block of 32 that holds such an output gets a NaN as its scale d.
  * Outputs must not overlap an input or each other.  T = 0 enqueues nothing.
  * Outputs are deterministic.  No workspace. */
 int lat_moe_dense_fp8(const void* x_fp8, const float* x_scales, const void* w_fp8, const float* w_scales, int64_t T,

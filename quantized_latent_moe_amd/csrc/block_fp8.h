@@ -117,6 +117,10 @@ __device__ __forceinline__ float amax8(const float* v) {
   return m;
 }
 
+// The larger value, or a NaN if one is (v_maximum3_f32): what a q8_1 block's
+// scale is made of, since its codes cannot hold a NaN.
+__device__ __forceinline__ float max_or_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // Largest value of each aligned group of 4 or 16 lanes, in all of its lanes.
 template <int LANES>
 __device__ __forceinline__ float group_max(float m) {

@@ -571,9 +571,9 @@ __global__ __launch_bounds__(64 * (WN * WT + NP)) void k_dense_fp8(const DenseAr
             float amax = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              amax = fmaxf(amax, fmaxf(fabsf(acc[2 * q][j][e]), fabsf(acc[2 * q + 1][j][e])));
-            amax = fmaxf(amax, __shfl_xor(amax, 16));
-            amax = fmaxf(amax, __shfl_xor(amax, 32));
+              amax = max_or_nan(amax, max_or_nan(fabsf(acc[2 * q][j][e]), fabsf(acc[2 * q + 1][j][e])));
+            amax = max_or_nan(amax, __shfl_xor(amax, 16));
+            amax = max_or_nan(amax, __shfl_xor(amax, 32));
             const float d = amax / 127.0f;
             const float id = d != 0.0f ? 1.0f / d : 0.0f;
             uint32_t pk[2];

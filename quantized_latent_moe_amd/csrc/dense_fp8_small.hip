@@ -218,7 +218,7 @@ __global__ __launch_bounds__(64 * small_waves(TF)) void k_dense_fp8_small(SmallA
         // 32 lanes hold one q8_1 block
         float amax = fabsf(v);
 #pragma unroll
-        for (int s = 1; s < 32; s <<= 1) amax = fmaxf(amax, __shfl_xor(amax, s));
+        for (int s = 1; s < 32; s <<= 1) amax = max_or_nan(amax, __shfl_xor(amax, s));
         const float d = amax / 127.0f;
         const float id = d != 0.0f ? 1.0f / d : 0.0f;
         const int q = round_half_away(v * id);
