@@ -130,6 +130,10 @@ enum Mode : int { kFast = 0, kExact = 1, kGated = 2, kGatedRaw = 3, kGatedExact 
 constexpr bool is_exact(int mode) { return mode == kExact || mode == kGatedExact || mode == kGatedRawExact; }
 // H is rounded where it is made.
 constexpr bool is_rounded(int mode) { return mode == kGated || mode == kGatedExact; }
+constexpr Fp8Product product_of(int mode) {
+  if (mode >= kGated) return is_exact(mode) ? kFp8GatedPairExact : kFp8GatedPair;
+  return is_exact(mode) ? kFp8DenseExact : kFp8Dense;
+}
 
 template <int FA, int FB, int WN, int WT, int MODE, int STAGES, int NP>
 struct Tile {
@@ -137,12 +141,8 @@ struct Tile {
   static constexpr int kWaves = WN * WT;                // that multiply; NP more load
   static constexpr int kThreads = 64 * (kWaves + NP);
   static constexpr int TN = 16 * FA * WN, TT = 16 * FB * WT;
-  // The workgroups of large tiles, of which a CU holds one, stay and take one
-  // tile after the other: the next tile's loads run while the last one's
-  // results are stored.  21000 tokens: 4096 x 1024 weights 107 us (128 with a
-  // workgroup a tile), 8192 x 2048 365 (430), 4096 x 4096 325 (342).  Smaller
-  // tiles overlap with the CU's other workgroup, and gain nothing.
-  static constexpr bool kPersistent = TN * TT >= 128 * 128;
+  // Whether the workgroups stay and take one tile after the other.
+  static constexpr bool kPersistent = Fp8Tile{TN, TT, GATED}.stays();
   static constexpr int kLoadsA = TN / 8 / NP, kLoadsB = TT / 8 / NP;  // 1 KB each
   static_assert(kFp8Block % (16 * FA) == 0, "a wave's weight rows lie in one scale block");
   static_assert(TN % (8 * NP) == 0 && TT % (8 * NP) == 0, "whole loads");
@@ -650,11 +650,13 @@ __global__ __launch_bounds__(64 * (WN * WT + NP)) void k_dense_fp8(const DenseAr
   }
 }
 
-template <int FA, int FB, int WN, int WT, int MODE, int STAGES, int NP>
+// V: the variant's place among its product's.
+template <int V, int FA, int FB, int WN, int WT, int MODE, int STAGES, int NP>
 hipError_t run(DenseArgs a, int num_cus, hipStream_t st) {
   using D = Tile<FA, FB, WN, WT, MODE, STAGES, NP>;
-  const int tn = D::GATED ? D::TN / 2 : D::TN;
-  a.n_nt = (a.N + tn - 1) / tn;
+  constexpr Fp8Tile tile = kFp8Tiles[product_of(MODE)][V];
+  static_assert(tile.rows == D::TN && tile.tokens == D::TT && tile.gated == D::GATED, "the tile that the choice knows");
+  a.n_nt = (a.N + tile.cols() - 1) / tile.cols();
   a.n_tt = (int)((a.T + D::TT - 1) / D::TT);
   // a launch holds fewer than 2^32 threads: tiles that are not persistent are
   // chosen for few tiles, or for N <= 64 with K >= 1920, of which memory holds
@@ -665,55 +667,6 @@ hipError_t run(DenseArgs a, int num_cus, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Choice of the tile.  Large tiles move fewer bytes through LDS for a product,
-// small ones fill the chip with few rows and leave less of its last pass idle.
-// The time of a variant is estimated from what one CU was measured to take for
-// a K step while it holds 1, 2, ... of the variant's tiles (us; the launch has
-// 256 CUs busy), for what a tile costs beside its steps, and for the start:
-// passes with every CU full, then one with the tiles that remain.
-struct Variant {
-  int cols, tokens;  // of a tile
-  int per_cu;        // tiles a CU holds (LDS)
-  float start, tile, step[2];
-};
-constexpr Variant kFastTiles[] = {{256, 128, 1, 3.f, 3.f, {0.86f}},
-                                  {128, 128, 1, 3.f, 2.f, {0.46f}},
-                                  {128, 64, 2, 0.f, 4.f, {0.32f, 0.65f}},
-                                  {64, 64, 2, 0.f, 3.f, {0.20f, 0.39f}}};
-constexpr Variant kExactTiles[] = {{128, 192, 1, 5.f, 2.f, {1.40f}},
-                                   {128, 128, 1, 4.f, 2.f, {0.92f}},
-                                   {64, 64, 2, 0.f, 4.f, {0.35f, 0.57f}}};
-constexpr Variant kGatedTiles[] = {{128, 128, 1, 4.f, 3.f, {0.86f}},
-                                   {128, 64, 1, 3.f, 2.f, {0.50f}},
-                                   // with the rounding in a launch of its own
-                                   {64, 64, 2, 3.f, 4.f, {0.32f, 0.65f}},
-                                   {32, 64, 2, 3.f, 3.f, {0.20f, 0.39f}}};
-// With exact products: H rounded, and fp32 H.  512 tokens of C = 4096, F = 2048
-// take 37.4 us for the whole block (27.5 with e4m3 products), 5268 with F = 8192
-// 913 us (553).
-constexpr Variant kGatedExactTiles[] = {{128, 64, 1, 4.f, 3.f, {0.95f}}, {32, 64, 2, 3.f, 4.f, {0.35f, 0.57f}}};
-// Variants that round H themselves come first, two and one.  128 columns of H are one scale's, so these
-// fill the chip only where T F is large: 65 tokens of C = 4096, F = 2048 (16
-// tiles of 128 x 64) took 24.0 us for the whole block, and take 16.9 us with
-// tiles of 32 columns, fp32 H and a launch that rounds it.
-constexpr int kGatedRounded = 2, kGatedExactRounded = 1;
-
-int pick(const Variant* v, int count, int64_t T, int N, int nb, int num_cus) {
-  int best = 0;
-  float least = 0.f;
-  for (int i = 0; i < count; ++i) {
-    const int64_t tiles = ((T + v[i].tokens - 1) / v[i].tokens) * ((N + v[i].cols - 1) / v[i].cols);
-    const int64_t slots = (int64_t)num_cus * v[i].per_cu, passes = tiles / slots, rest = tiles % slots;
-    float t = v[i].start + (float)passes * (v[i].step[v[i].per_cu - 1] * (float)nb + v[i].tile);
-    if (rest) t += v[i].step[(rest + num_cus - 1) / num_cus - 1] * (float)nb + v[i].tile;
-    if (i == 0 || t < least) {
-      best = i;
-      least = t;
-    }
-  }
-  return best;
-}
-
 }  // namespace
 
 hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int64_t T, int N,
@@ -721,35 +674,33 @@ hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w,
                             hipStream_t st) {
   const DenseArgs a{x, xs, w, ws, y_f32, y_bf16, y_q8, nullptr, nullptr, T, N, K, (K + kStep - 1) / kStep, 0, 0};
   if (exact) {
-    switch (pick(kExactTiles, 3, T, N, a.nb, num_cus)) {
-      case 0: return run<4, 3, 2, 4, kExact, 3, 4>(a, num_cus, st);
-      case 1: return run<4, 4, 2, 2, kExact, 3, 2>(a, num_cus, st);
-      default: return run<2, 2, 2, 2, kExact, 4, 4>(a, num_cus, st);
+    switch (fp8_pick_tile(kFp8DenseExact, T, N, a.nb, num_cus)) {
+      case 0: return run<0, 4, 3, 2, 4, kExact, 3, 4>(a, num_cus, st);
+      case 1: return run<1, 4, 4, 2, 2, kExact, 3, 2>(a, num_cus, st);
+      default: return run<2, 2, 2, 2, 2, kExact, 4, 4>(a, num_cus, st);
     }
   }
-  switch (pick(kFastTiles, 4, T, N, a.nb, num_cus)) {
-    case 0: return run<4, 4, 4, 2, kFast, 3, 4>(a, num_cus, st);
-    case 1: return run<4, 4, 2, 2, kFast, 3, 4>(a, num_cus, st);
-    case 2: return run<4, 2, 2, 2, kFast, 3, 2>(a, num_cus, st);
-    default: return run<2, 2, 2, 2, kFast, 4, 4>(a, num_cus, st);
+  switch (fp8_pick_tile(kFp8Dense, T, N, a.nb, num_cus)) {
+    case 0: return run<0, 4, 4, 4, 2, kFast, 3, 4>(a, num_cus, st);
+    case 1: return run<1, 4, 4, 2, 2, kFast, 3, 4>(a, num_cus, st);
+    case 2: return run<2, 4, 2, 2, 2, kFast, 3, 2>(a, num_cus, st);
+    default: return run<3, 2, 2, 2, 2, kFast, 4, 4>(a, num_cus, st);
   }
 }
 
 hipError_t launch_gateup_fp8(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int64_t T, int F,
                              int C, bool exact, float* h32, uint8_t* h, float* hs, int num_cus, hipStream_t st) {
   const DenseArgs a{x, xs, gu, gus, h32, nullptr, nullptr, h, hs, T, F, C, (C + kStep - 1) / kStep, 0, 0};
-  const bool raw = T * F <= kFp8H32;
+  const int variant = fp8_pick_tile(exact ? kFp8GatedPairExact : kFp8GatedPair, T, F, a.nb, num_cus);
   hipError_t e;
   if (exact) {
-    if (pick(kGatedExactTiles, raw ? 2 : kGatedExactRounded, T, F, a.nb, num_cus) < kGatedExactRounded)
-      return run<4, 2, 4, 2, kGatedExact, 3, 4>(a, num_cus, st);
-    e = run<2, 2, 2, 2, kGatedRawExact, 4, 4>(a, num_cus, st);
+    if (variant == 0) return run<0, 4, 2, 4, 2, kGatedExact, 3, 4>(a, num_cus, st);
+    e = run<1, 2, 2, 2, 2, kGatedRawExact, 4, 4>(a, num_cus, st);
   } else {
-    const int variant = pick(kGatedTiles, raw ? 4 : kGatedRounded, T, F, a.nb, num_cus);
-    if (variant == 0) return run<4, 4, 4, 2, kGated, 3, 4>(a, num_cus, st);
-    if (variant == 1) return run<8, 2, 2, 2, kGated, 3, 4>(a, num_cus, st);
-    e = variant == 2 ? run<4, 2, 2, 2, kGatedRaw, 3, 2>(a, num_cus, st)
-                     : run<2, 2, 2, 2, kGatedRaw, 4, 4>(a, num_cus, st);
+    if (variant == 0) return run<0, 4, 4, 4, 2, kGated, 3, 4>(a, num_cus, st);
+    if (variant == 1) return run<1, 8, 2, 2, 2, kGated, 3, 4>(a, num_cus, st);
+    e = variant == 2 ? run<2, 4, 2, 2, 2, kGatedRaw, 3, 2>(a, num_cus, st)
+                     : run<3, 2, 2, 2, 2, kGatedRaw, 4, 4>(a, num_cus, st);
   }
   return e == hipSuccess ? launch_quantize_fp8(h32, LAT_MOE_F32, T, F, h, hs, st) : e;
 }

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/lat_moe.h"
+#include "fp8_tiles.h"
 
 namespace latmoe {
 
@@ -275,9 +276,7 @@ hipError_t launch_gateup_fp8_small(const uint8_t* x, const float* xs, const uint
                                    int F, int C, float* h, hipStream_t st);
 // Gate and up projections (gu [2F][C]: gate rows, then up rows), silu(G) * U,
 // rounded to e4m3 rows h [T][F].  Up to kFp8H32 values of H may take the way
-// through h32 [T][F] (not read before it is written): with more, tiles of 128
-// columns and 64 tokens are on half of the CUs and their rounding costs no launch.
-constexpr int64_t kFp8H32 = (int64_t)1 << 20;
+// through h32 [T][F] (not read before it is written).
 hipError_t launch_gateup_fp8(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int64_t T, int F,
                              int C, bool exact, float* h32, uint8_t* h, float* hs, int num_cus, hipStream_t st);
 
