@@ -367,7 +367,8 @@ __global__ __launch_bounds__(64 * (WN * WT + NP)) void k_dense_fp8(const DenseAr
   const int K = a.K, nb = a.nb;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int first = (int)blockIdx.x;
+  const int first = (int)workgroup_number();
+  if (!D::kPersistent && first >= a.n_nt * a.n_tt) return;  // the whole workgroup
   const int stride = D::kPersistent ? (int)gridDim.x : 1, items = D::kPersistent ? a.n_nt * a.n_tt : first + 1;
 
   if (wave >= D::kWaves) {
@@ -658,12 +659,9 @@ hipError_t run(DenseArgs a, int num_cus, hipStream_t st) {
   static_assert(tile.rows == D::TN && tile.tokens == D::TT && tile.gated == D::GATED, "the tile that the choice knows");
   a.n_nt = (a.N + tile.cols() - 1) / tile.cols();
   a.n_tt = (int)((a.T + D::TT - 1) / D::TT);
-  // a launch holds fewer than 2^32 threads: tiles that are not persistent are
-  // chosen for few tiles, or for N <= 64 with K >= 1920, of which memory holds
-  // fewer than 2^22
-  const int items = a.n_nt * a.n_tt, grid = D::kPersistent ? std::min(items, num_cus) : items;
-  hipLaunchKernelGGL((k_dense_fp8<FA, FB, WN, WT, MODE, STAGES, NP>), dim3((unsigned)grid), dim3(D::kThreads), 0, st,
-                     a);
+  const int items = a.n_nt * a.n_tt;
+  const dim3 grid = grid_of(D::kPersistent ? std::min(items, num_cus) : items);
+  hipLaunchKernelGGL((k_dense_fp8<FA, FB, WN, WT, MODE, STAGES, NP>), grid, dim3(D::kThreads), 0, st, a);
   return hipGetLastError();
 }
 

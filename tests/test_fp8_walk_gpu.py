@@ -75,3 +75,29 @@ def test_gated(product, tile, T, F, C):
     ref, mag = fp8.dense(h, s, d, ds)
     tol = _tol(ref, mag, F) + (0.0 if exact else _cut(h, s, d, ds))
     assert (np.abs(b.float().cpu().numpy()[t] - ref) <= tol * (1 + 2.0 ** -8) + np.abs(ref) * 2.0 ** -8).all()
+
+
+@pytest.mark.parametrize("exact", [True, False])
+def test_more_tiles_than_one_row_of_the_grid(exact):
+    """More than 2^20 workgroups of a tile each come in rows of 2^20: many tokens
+    by one weight row, tokens of which a pattern of 4096 repeats."""
+    T, N, K, n = (1 << 26) + 77, 1, 2064, 4096
+    c = _tiles.choose(_tiles.DENSE_EXACT if exact else _tiles.DENSE, T, N, K)
+    assert not c.stays and c.tiles > 1 << 20
+    rng = np.random.default_rng(1)
+    (x, xs), (w, ws) = _x(rng, n, K), _w(rng, N, K)
+    xd, xsd, wd, wsd = (_dev(a) for a in (x, xs, w, ws))
+    whole = T // n * n
+    X, XS = torch.empty((T, K), dtype=torch.uint8, device="cuda"), torch.empty((T, xs.shape[1]), device="cuda")
+    for big, small in ((X, xd.view(torch.uint8)), (XS, xsd)):
+        big[:whole].view(whole // n, n, -1).copy_(small.expand(whole // n, n, -1))
+        big[whole:] = small[:T - whole]
+    y = torch.full((T, N), float("nan"), device="cuda")
+    lm.dense_fp8(X.view(F8), XS, wd, wsd, y_f32=y, exact=exact)
+    torch.cuda.synchronize()
+    first = y[:n]
+    assert (y[:whole].view(-1, n, N) == first).all() and torch.equal(y[whole:], first[:T - whole])
+    ref, mag = fp8.dense(x, xs, w, ws)
+    assert (np.abs(first.cpu().numpy() - ref) <= _tol(ref, mag, K) + (0.0 if exact else _cut(x, xs, w, ws))).all()
+    del X, XS, y, first
+    torch.cuda.empty_cache()
