@@ -377,12 +377,11 @@ int lat_moe_rmsnorm(const void* x, int32_t x_type, const void* residual, int32_t
     if (!aligned16(p)) return LAT_MOE_EINVAL;  // null counts as aligned
   // in place only where an element's place stays its own
   if (y && y == x && y_type != x_type) return LAT_MOE_EINVAL;
-  int num_cus = 1;
-  int rc = check_device(&num_cus);
+  int rc = check_device(nullptr);
   if (rc != LAT_MOE_OK) return rc;
   const NormArgs a{x, residual, weight, residual_out, y, static_cast<uint8_t*>(y_q8_1), static_cast<uint8_t*>(y_fp8),
                    y_scales, T, C, x_type, residual_type, y_type, eps, 1.0 / C};
-  if (launch_rmsnorm(a, num_cus, static_cast<hipStream_t>(stream)) != hipSuccess) return LAT_MOE_ELAUNCH;
+  if (launch_rmsnorm(a, static_cast<hipStream_t>(stream)) != hipSuccess) return LAT_MOE_ELAUNCH;
   return LAT_MOE_OK;
 }
 

@@ -31,7 +31,6 @@
 namespace latmoe {
 namespace {
 
-
 struct SmallArgs {
   const uint8_t* x;  // [T][K] e4m3, or null: the rows are h32
   const float* xs;
@@ -60,19 +59,19 @@ __device__ __forceinline__ void widen16(const uint4* p, v8bf* o) {
 // rounds them again, which for few tokens costs less than a launch between).
 enum SmallMode : int { kRows = 0, kGatedPair = 1, kRound = 2 };
 
-// Token columns past T and weight rows past N hold zeros or a clamped row;
-// they meet only results that are not stored.
 // Waves of a workgroup, each with TF blocks in flight.  For 16 tokens 16 waves
 // with one block each take 3.0 us for 4096 x 1024 weights and 4.8 us for
 // 8192 x 2048, eight with four each 3.6 and 5.7 us (the wave's own chain of
 // blocks is as long, and few blocks leave it waiting for the last).
 constexpr int small_waves(int tf) { return tf == 1 ? 16 : 8; }
 
+// Token columns past T and weight rows past N hold zeros or a clamped row;
+// they meet only results that are not stored.
 template <int FR, int TF, int MODE>
 __global__ __launch_bounds__(64 * small_waves(TF)) void k_dense_fp8_small(SmallArgs a) {
   constexpr bool GATED = MODE == kGatedPair;
   constexpr int kWaves = small_waves(TF), U = TF;  // U blocks in flight per wave
-  constexpr int NF = GATED ? 8 : 16 * FR;              // output columns
+  constexpr int NF = GATED ? 8 : 16 * FR;          // output columns
   static_assert(!GATED || FR == 1, "one fragment of gate and up rows");
   static_assert(MODE != kRound || TF == 1, "rounding for 16 tokens");
   __shared__ __align__(16) float red[kWaves][FR * TF][64][4];

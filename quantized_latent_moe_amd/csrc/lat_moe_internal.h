@@ -252,7 +252,7 @@ struct NormArgs {
   float eps;
   double inv_c;  // 1 / C
 };
-hipError_t launch_rmsnorm(const NormArgs& a, int num_cus, hipStream_t st);
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st);
 // e4m3 rows [T][K] x e4m3 weights [N][K] -> y in fp32, bf16 and/or q8_1 (any may be null, not all).
 // exact: products by the bf16 MFMA.
 hipError_t launch_dense_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, int64_t T, int N,

@@ -201,7 +201,7 @@ void run_rmsnorm(const NormArgs& a, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_rmsnorm(const NormArgs& a, int num_cus, hipStream_t st) {
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st) {
   if (a.C <= 512) run_rmsnorm<64, 1>(a, st);
   else if (a.C <= 2048) run_rmsnorm<256, 1>(a, st);
   else if (a.C <= 4096) run_rmsnorm<256, 2>(a, st);
