@@ -178,3 +178,51 @@ def test_c_entry_points_without_a_choice():
         assert lm.lib().lat_moe_dense_fp8(p(a[0]), p(a[1]), p(a[2]), p(w), T, 2 * F, C, *o, st) == 0
         torch.cuda.synchronize()
         assert torch.equal(*z)
+
+
+@pytest.mark.parametrize("T", [16, 40, 700])
+def test_subnormal_codes(T):
+    """Products of the smallest codes, subnormal ones among them: whole numbers of
+    2^-18 with few bits, which add up exactly."""
+    rng = np.random.default_rng(T)
+    N, K = 160, 272
+    x = (rng.integers(0, 12, (T, K)) | rng.choice([0, 128], (T, K))).astype(np.uint8)
+    w = (rng.integers(0, 12, (N, K)) | rng.choice([0, 128], (N, K))).astype(np.uint8)
+    xs, ws = np.ones((T, fp8.blocks(K)), np.float32), np.ones((fp8.blocks(N), fp8.blocks(K)), np.float32)
+    d = tuple(_dev(a) for a in (x, xs, w, ws))
+    ref = fp8.decode(x) @ fp8.decode(w).T
+    # all codes have the same exponent as the operand holds it: nothing is cut
+    for exact in (True, False):
+        y = _call_dense(d, T, N, exact, f32=True)[0]
+        assert np.array_equal(y.cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("T,C,F", [(40, 272, 400), (700, 400, 2064)])
+def test_exact_calls_captured(T, C, F):
+    """The gated block and a projection with exact products in a graph, replayed
+    between eager calls of other products on the same workspace."""
+    rng = np.random.default_rng(T)
+    a = tuple(_dev(v) for v in _ffn_inputs(rng, T, C, F))
+    w, ws = (_dev(v) for v in _w(rng, 96, C))
+    work = torch.empty(lm.ffn_fp8_workspace_size(T, C, F), dtype=torch.uint8, device="cuda")
+    out = [torch.empty(T, C, device="cuda"), torch.empty(T, 3, 36, dtype=torch.uint8, device="cuda")]
+
+    def step():
+        lm.ffn_fp8(*a, work, y_f32=out[0], exact=True)
+        lm.dense_fp8(*a[:2], w, ws, y_q8_1=out[1], exact=True)
+
+    step()
+    torch.cuda.synchronize()
+    eager = [o.clone() for o in out]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    other = torch.empty(T, C, dtype=torch.bfloat16, device="cuda")
+    for _ in range(4):
+        for o in out:
+            o.zero_()
+        work.fill_(0xFF)
+        lm.ffn_fp8(*a, work, y_bf16=other, exact=False)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, e) for o, e in zip(out, eager))
