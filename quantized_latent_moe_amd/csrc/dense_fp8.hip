@@ -7,7 +7,7 @@
 //
 // One MFMA covers exactly one block of K = 128, so its result with a zero
 // accumulator input is P, and one fp32 FMA an element folds it into y: four
-// VALU operations for each 16-pass MFMA, which run beside the next MFMAs.
+// VALU operations for each MFMA of 8 passes (32 cycles), beside the next MFMAs.
 //
 // The e4m3 MFMA adds products in groups of eight neighbours in K, each cut
 // (toward zero) to a multiple of 2^-13 of the power of two of the group's
@@ -18,33 +18,38 @@
 // cancel and small ones beside them are what is left, and where a rounding to
 // few bits follows: in the gated block 0.24% of H's codes become their
 // neighbours, which are as near, and that moves y by 1.2e-3 of its norm (H's
-// rounding itself by 2.3e-2, with either products).  Exact products, which the fp32 y of a projection
-// takes unless the call says otherwise: the codes are widened to bf16 in
-// registers (two a VALU operation), and four bf16 MFMAs a block take twice the
-// matrix time.
+// rounding itself by 2.3e-2, with either products).  Exact products, which the
+// fp32 y of a projection takes unless the call says otherwise (y is then off by
+// 1e-7 of its norm at K = 4096): the codes are widened to bf16 in registers (two
+// a VALU operation), and four bf16 MFMAs a block take twice the matrix time.
 //
 // One workgroup computes TN = 16 FA WN weight rows x TT = 16 FB WT tokens.
 // Weights are the MFMA's row operand: a lane then holds four neighbouring
 // weight rows of one token, one scale for a whole MFMA result.  NP waves only
 // load: per K step of 128 both tiles go to LDS by direct loads (16 bytes a
 // lane, no registers), STAGES steps ahead; a row is 128 bytes, its 16-byte
-// chunks XOR-swizzled by the row so that a fragment read touches every bank
-// once (the swizzle is applied to the global address of a lane, since the LDS
-// side of a direct load is linear).  WN x WT waves multiply: each reads its
+// chunks XOR-swizzled by the row so that fragment reads have no bank conflicts
+// (none counted; the swizzle is applied to the global address of a lane, since
+// the LDS side of a direct load is linear).  Scale reads, whose lanes are 16
+// bytes apart, have eight conflict cycles a wave and step, a tenth of LDS's.  WN x WT waves multiply: each reads its
 // fragments a step ahead into the registers that their last MFMA has left, so
 // that no LDS latency stands between two steps, and one barrier a step joins
 // all waves.  (A wave that loads and multiplies waits for the memory pipe to
 // take each load, 20 cycles for each of all the waves' loads, and its MFMAs
 // with it: 128 x 128 tiles took 0.7 us a step that way and take 0.47 us now.)
 //
-// What bounds it: direct loads reach about 100 GB/s a CU, 0.48 us for a step
-// of 256 x 128, and the MFMAs of that step take 0.5 to 0.57 us (the clock
-// falls to 1.8 GHz under them); together, with the LDS reads between, 0.86 us.  A
-// small tile's step is its loads: 0.20 us for the 16 KB of 64 x 64 on one CU,
-// and 8 stages instead of 4, a barrier for two steps or a second set of
-// fragment registers leave it there.  21000 x 4096 rows by
-// 4096 weights take 347 us (2030 TF; as much through the bf16 MFMA with an fp32
-// y 640 us, 1100 TF).
+// What bounds it: a step of 256 x 128 takes 1700 cycles of a CU, 0.86 to 1 us as
+// the clock falls to 1.7 to 2 GHz under it, and no unit is busy all of them: the
+// MFMAs need 1024 (the matrix pipe is counted busy 60% of the cycles), the LDS
+// reads 640 (38%; fragment reads alone run at 244 bytes a cycle, 128 KB in
+// 0.26 us), and the direct loads alone take 0.36 us (132 GB/s a CU where L2 has
+// the rows), 0.39 together with the reads.  So neither LDS nor loads are the
+// bound; what is left stands at the step's barrier, where all waves of the CU
+// wait for the slowest.  A small tile's step is its loads: 0.20 us for the 16 KB
+// of 64 x 64 on one CU, and 8 stages instead of 4, a barrier for two steps or a
+// second set of fragment registers leave it there.  21000 x 4096 rows by 4096
+// weights take 330 to 360 us (2000 to 2130 TF; with exact products 620 to
+// 690 us, 1020 to 1130 TF), the range of several runs.
 #include <algorithm>
 #include <type_traits>
 

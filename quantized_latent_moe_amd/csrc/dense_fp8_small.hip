@@ -13,8 +13,11 @@
 //
 // What bounds it: launch, the latency of one or two reads in a row, and the
 // adding of partial sums; then the weights' rate.  In a captured graph a
-// product of 4 tokens takes 3.0 us for 4096 x 1024 weights, 5.3 us for
-// 4096 x 4096 (16 MB, 3.2 TB/s) and 5.1 us for 8192 x 2048.
+// product of 4 tokens takes 2.9 us for 4096 x 1024 weights, 4.8 us for
+// 1024 x 4096 (64 workgroups, two blocks of K a wave), 5.3 us for 4096 x 4096
+// (16 MB, 3.2 TB/s), 14 us for 8192 x 8192 and 25 us for 16384 x 8192 (5.4 TB/s).
+// With a q8_1 output, whose blocks are 32 columns, a workgroup takes 32 weight
+// rows: 7.6 us for 1024 x 4096.
 //
 // Against the tiles (us, 16 | 17 .. 32 tokens here and in tiles):
 //   4096 x 4096:  7.0 | 7.8 .. 9.6, bf16 tiles 8.7, fp32 (exact) tiles 13.4

@@ -25,9 +25,10 @@ struct Fp8Tile {
   constexpr int cols() const { return gated ? rows / 2 : rows; }
   // The workgroups of large tiles, of which a CU holds one, stay and take one
   // tile after the other: the next tile's loads run while the last one's
-  // results are stored.  21000 tokens: 4096 x 1024 weights 107 us (128 with a
-  // workgroup a tile), 8192 x 2048 365 (430), 4096 x 4096 325 (342).  Smaller
-  // tiles overlap with the CU's other workgroup, and gain nothing.
+  // results are stored.  21000 tokens, bf16: 4096 x 1024 weights 119 us (142 with
+  // a workgroup a tile, timed in turn), 8192 x 2048 370 (434), 4096 x 4096 336
+  // (353); exact products to fp32 655 (682).  Smaller tiles overlap with the CU's
+  // other workgroup, and gain nothing.
   constexpr bool stays() const { return rows * tokens >= 128 * 128; }
   int64_t count(int64_t T, int N) const { return (T + tokens - 1) / tokens * (((int64_t)N + cols() - 1) / cols()); }
 };
