@@ -101,3 +101,26 @@ def test_more_tiles_than_one_row_of_the_grid(exact):
     assert (np.abs(first.cpu().numpy() - ref) <= _tol(ref, mag, K) + (0.0 if exact else _cut(x, xs, w, ws))).all()
     del X, XS, y, first
     torch.cuda.empty_cache()
+
+
+def test_exact_gated_offsets_beyond_32_bits():
+    """H past 2^32 values, rounded where it is made with exact products: the last
+    rows are those of a call of their own."""
+    T, C, F = 140003, 144, 32768
+    g = torch.Generator(device="cuda").manual_seed(1)
+    codes = lambda *s: torch.randint(0, 0x7E, s, dtype=torch.uint8, device="cuda", generator=g).view(F8)
+    scales = lambda *s: torch.rand(s, device="cuda", generator=g) * 1e-3
+    x, xs, gu, gus = codes(T, C), scales(T, 2), codes(2 * F, C), scales(2, F // 128, 2)
+    d, ds = codes(C, F), scales(2, F // 128)
+    at = T // 4 * 4 - 10000
+    out = []
+    for first in (0, at):
+        n = T - first
+        h, hs = torch.full((n, F), 0x7F, dtype=torch.uint8, device="cuda").view(F8), torch.full((n, F // 128), float("nan"), device="cuda")
+        y = torch.full((n, C), float("nan"), device="cuda")
+        work = torch.empty(lm.ffn_fp8_workspace_size(n, C, F), dtype=torch.uint8, device="cuda")
+        lm.ffn_fp8(x[first:], xs[first:], gu, gus, d, ds, work, y_f32=y, h_fp8=h, h_scales=hs, exact=True)
+        torch.cuda.synchronize()
+        out.append((h.view(torch.uint8)[at - first:].clone(), hs[at - first:].clone(), y[at - first:].clone()))
+        assert torch.isfinite(hs).all() and torch.isfinite(y).all() and not (h.view(torch.uint8)[::97] & 0x7F == 0x7F).any()
+    assert all(torch.equal(a, b) for a, b in zip(*out))
