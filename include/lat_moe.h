@@ -258,6 +258,49 @@ int lat_moe_dense_q4_0_debug(const void* x_q8_1, const void* w_q4_0, int64_t T, 
 int lat_moe_router_topk(const float* logits, int64_t T, int32_t E, int32_t k, int32_t* router_idx, float* router_w,
                         void* stream);
 
+/* Routing rules of lat_moe_router_topk_ex. */
+#define LAT_MOE_SCORE_SOFTMAX 0 /* s = softmax of the row's logits */
+#define LAT_MOE_SCORE_SIGMOID 1 /* s = 1 / (1 + exp(-logit)) */
+#define LAT_MOE_GROUP_MAX 0     /* a group's score is its largest candidate */
+#define LAT_MOE_GROUP_TOP2 1    /* ... the sum of its two largest */
+#define LAT_MOE_ROUTER_MAX_GROUPS 64
+typedef struct lat_moe_routing {
+  int32_t score;       /* LAT_MOE_SCORE_* */
+  int32_t groups;      /* E / groups neighbouring experts each; 1: no groups */
+  int32_t top_groups;  /* groups a token may pick from */
+  int32_t group_score; /* LAT_MOE_GROUP_* (not looked at where top_groups == groups) */
+  int32_t renormalise; /* nonzero: the weights are divided by their sum */
+  float scale;         /* what the weights are multiplied by */
+} lat_moe_routing;
+
+/* Router with a choice of scores, a bias for balance, groups and scaled
+ * weights:
+ *     s[e] = softmax or sigmoid of the logits, in 64 bits, rounded once to fp32
+ *     c[e] = s[e] + bias[e]                                              (fp32)
+ *     the top_groups groups with the largest group scores (equal: lower group)
+ *     the k largest c among these groups' experts, descending (equal: lower id)
+ *     w[j] = scale * s of pick j, or scale * s / (sum of the picks' s)
+ * The bias decides which experts are picked and does not enter the weights.
+ * Weights and their sum are in 64 bits, rounded once.
+ * An expert whose logit is -inf or NaN, or whose bias is, is closed: its c is
+ * the lowest finite fp32, its weight 0 where it is picked for lack of others
+ * (a row without any open expert picks the lowest ids with weights 0), and the
+ * second of a group's two largest counts as 0 where it is closed.  A logit of
+ * +inf counts as the largest finite fp32, and so does a larger c.
+ *   logits      [T][E] fp32
+ *   bias        [E] fp32, or NULL
+ *   routing     host memory, read during the call
+ *   router_idx  [T][k] int32 out, router_w [T][k] fp32 out
+ * Supported: T >= 0, T < 2^31, 1 <= E <= LAT_MOE_ROUTER_MAX_E, E % groups == 0,
+ * 1 <= groups <= LAT_MOE_ROUTER_MAX_GROUPS, 1 <= top_groups <= groups, at least
+ * two experts a group where TOP2 is looked at, 1 <= k <= min(top_groups * E /
+ * groups, LAT_MOE_ROUTER_MAX_K), scale finite; pointers 16-byte aligned.
+ * T = 0 enqueues nothing.  Outputs are deterministic.  lat_moe_router_topk
+ * ranks by the logits themselves: logits so near that their scores round to
+ * one fp32 are in the order of their ids here, and in the logits' order there. */
+int lat_moe_router_topk_ex(const float* logits, const float* bias, int64_t T, int32_t E, int32_t k,
+                           const lat_moe_routing* routing, int32_t* router_idx, float* router_w, void* stream);
+
 /* ---- 8-bit floating point with a scale for each block of 128 ----
  *
  * Beside q8_1 the library takes activations as e4m3 rows and dense weights as
@@ -396,6 +439,67 @@ int lat_moe_ffn_fp8_ex(const void* x_fp8, const float* x_scales, const void* gat
                        const void* down_fp8, const float* down_scales, int64_t T, int32_t C, int32_t F, float* y_f32,
                        void* y_bf16, void* h_fp8, float* h_scales, int32_t products, void* workspace,
                        size_t workspace_bytes, void* stream);
+
+/* ---- rows and weights in 16 bits ----
+ *
+ * Dense products for packs that keep a projection, the router's matrix or a
+ * shared expert in bf16 or fp16. */
+#define LAT_MOE_DENSE_16_MAX_N (1 << 20)      /* weight rows of one matrix */
+#define LAT_MOE_DENSE_16_MAX_STRIDE (1 << 20) /* elements between two rows of x */
+
+/* Activations, in fp32:
+ *   NONE v;  RELU max(v, 0), a NaN stays one;  SILU v / (1 + exp(-v));
+ *   GELU v (1 + erf(v / sqrt 2)) / 2, within 1e-7 |v|;
+ *   GELU_TANH v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+#define LAT_MOE_ACT_NONE 0
+#define LAT_MOE_ACT_RELU 1
+#define LAT_MOE_ACT_SILU 2
+#define LAT_MOE_ACT_GELU 3
+#define LAT_MOE_ACT_GELU_TANH 4
+
+/* Dense projection of 16-bit rows with 16-bit weights (the router's logits, a
+ * latent D or U projection, any other projection of a layer), with bias,
+ * activation and residual:
+ *     y[t][n] = act(sum over k of x[t][k] * w[n][k] + bias[n]) + residual[t][n]
+ * Products are exact and added in fp32; what follows is in fp32 and rounded
+ * once.
+ *   x         [T][K] of `type` (LAT_MOE_BF16 or LAT_MOE_F16), rows x_stride
+ *             elements apart (a multiple of 8, K <= x_stride <=
+ *             LAT_MOE_DENSE_16_MAX_STRIDE)
+ *   w         [N][K] of `type`, without gaps
+ *   bias      [N] fp32, or NULL
+ *   residual  [T][N] of residual_type, rows residual_stride >= N elements
+ *             apart, or NULL; may be y itself (same type and stride)
+ *   y         [T][N] of y_type, rows y_stride >= N elements apart, or NULL
+ *   y_q8_1    [T][N/32] q8_1 blocks of the fp32 y (N % 32 == 0), or NULL: the
+ *             latent rows the expert stage reads
+ * At least one of y and y_q8_1 must be given; the type and stride of an array
+ * that is NULL are not looked at.  Supported: T >= 0, T < 2^31, 1 <= N <=
+ * LAT_MOE_DENSE_16_MAX_N, K % 8 == 0, 8 <= K <= 65536, ceil(T/64) *
+ * ceil(N/64) < 2^31, strides < 2^31; pointers 16-byte aligned.  y and residual are read
+ * and written 16 bytes at a time where N and their strides are multiples of 8.
+ * A NaN or an infinity in x, w, bias or residual reaches the outputs that it
+ * enters and no others; a q8_1 block of 32 that holds a NaN output gets a NaN
+ * as its scale d.  Beyond the case named, outputs must not overlap an input or
+ * each other; what lies between the rows of y stays as it is.  T = 0 enqueues
+ * nothing.  Outputs are deterministic.  No workspace. */
+int lat_moe_dense_16(const void* x, int64_t x_stride, const void* w, int32_t type, int64_t T, int32_t N, int32_t K,
+                     const float* bias, int32_t activation, const void* residual, int32_t residual_type,
+                     int64_t residual_stride, void* y, int32_t y_type, int64_t y_stride, void* y_q8_1, void* stream);
+
+/* Gate and up projections of a gated feed-forward block in 16 bits (a layer's
+ * dense block, or a shared expert beside the routed ones):
+ *     h[t][f] = act(x[t] . w[f] + bias[f]) * (x[t] . w[F + f] + bias[F + f])
+ * in fp32, rounded once; lat_moe_dense_16 with a residual is the block's other
+ * half.
+ *   x     [T][K] of `type`, rows x_stride elements apart, as for lat_moe_dense_16
+ *   w     [2F][K] of `type`: gate rows 0..F-1, then the up rows
+ *   bias  [2F] fp32, or NULL
+ *   h     [T][F] of h_type, rows h_stride >= F elements apart
+ * Supported: as lat_moe_dense_16 with N = 2F.  h must not overlap an input.
+ * T = 0 enqueues nothing.  Outputs are deterministic.  No workspace. */
+int lat_moe_gated_16(const void* x, int64_t x_stride, const void* w, int32_t type, int64_t T, int32_t F, int32_t K,
+                     const float* bias, int32_t activation, void* h, int32_t h_type, int64_t h_stride, void* stream);
 
 /* Static description of an error code. */
 const char* lat_moe_strerror(int code);

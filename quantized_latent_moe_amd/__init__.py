@@ -35,6 +35,7 @@ EXPORTED = (
     "lat_moe_dense_q4_0",
     "lat_moe_dense_q4_0_debug",
     "lat_moe_router_topk",
+    "lat_moe_router_topk_ex",
     "lat_moe_quantize_fp8",
     "lat_moe_rmsnorm",
     "lat_moe_dense_fp8",
@@ -42,6 +43,8 @@ EXPORTED = (
     "lat_moe_ffn_fp8_workspace_size",
     "lat_moe_ffn_fp8",
     "lat_moe_ffn_fp8_ex",
+    "lat_moe_dense_16",
+    "lat_moe_gated_16",
     "lat_moe_strerror",
     "lat_moe_version",
 )
@@ -67,6 +70,11 @@ class Debug(ctypes.Structure):
         ("stage_events", ctypes.POINTER(ctypes.c_void_p)),
         ("deterministic", ctypes.c_int32),
     ]
+
+
+class Routing(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class LatMoeError(RuntimeError):
@@ -126,6 +134,12 @@ def lib() -> ctypes.CDLL:
         c.lat_moe_ffn_fp8.restype = ctypes.c_int
         c.lat_moe_ffn_fp8_ex.argtypes = [P, P, P, P, P, P, i64, i32, i32, P, P, P, P, i32, P, size, P]
         c.lat_moe_ffn_fp8_ex.restype = ctypes.c_int
+        c.lat_moe_router_topk_ex.argtypes = [P, P, i64, i32, i32, ctypes.POINTER(Routing), P, P, P]
+        c.lat_moe_router_topk_ex.restype = ctypes.c_int
+        c.lat_moe_dense_16.argtypes = [P, i64, P, i32, i64, i32, i32, P, i32, P, i32, i64, P, i32, i64, P, P]
+        c.lat_moe_dense_16.restype = ctypes.c_int
+        c.lat_moe_gated_16.argtypes = [P, i64, P, i32, i64, i32, i32, P, i32, P, i32, i64, P]
+        c.lat_moe_gated_16.restype = ctypes.c_int
         c.lat_moe_strerror.argtypes = [ctypes.c_int]
         c.lat_moe_strerror.restype = ctypes.c_char_p
         c.lat_moe_version.restype = ctypes.c_int
@@ -451,6 +465,138 @@ def ffn_fp8(x_fp8, x_scales, gateup_fp8, gateup_scales, down_fp8, down_scales, w
                                                                         dev),
                                   _products(exact), _tensor("workspace", workspace, u8, (nbytes,), dev), nbytes,
                                   raw(dev) if stream is None else int(stream))
+    if rc:
+        _check(rc)
+
+
+# ---- routing by other rules ----
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
+
+
+def _int32():
+    import torch
+    return torch.int32
+
+
+def _choice(name: str, value, choices) -> int:
+    code = choices.get(value)
+    if code is None:
+        raise ValueError(f"{name} has to be one of {', '.join(choices)}, got {value!r}")
+    return code
+
+
+def router_topk_ex(logits, k: int, router_idx, router_w, *, bias=None, score: str = "softmax", groups: int = 1,
+                   top_groups: Optional[int] = None, group_score: str = "top2", renormalise: bool = True,
+                   scale: float = 1.0, stream=None) -> None:
+    """float32 logits [T, E] -> top-k expert ids (int32 [T, k]) and weights
+    (float32 [T, k]) by scores with a choice of rules: softmax or sigmoid of
+    the logits; experts ranked by score + bias (float32 [E]; it does not enter
+    the weights); picks from the top_groups best of `groups` groups of
+    neighbouring experts, a group ranked by its largest candidate ("max") or
+    the sum of its two largest ("top2"); weights divided by their sum if
+    renormalise, and multiplied by scale.  Logits or biases of -inf close an
+    expert."""
+    _, f32, _, _, _, cur, raw = _torch()
+    if logits.dim() != 2:
+        raise ValueError("logits have to be 2-dimensional")
+    T, E = shape = logits.shape
+    dev = _device("logits", logits, cur)
+    if max(E, k, groups, top_groups or 0) >> 31:
+        raise ValueError("sizes beyond 32 bits")
+    rules = Routing(_choice("score", score, SCORES), groups, groups if top_groups is None else top_groups,
+                    _choice("group_score", group_score, GROUP_SCORES), renormalise, scale)
+    rc = lib().lat_moe_router_topk_ex(_tensor("logits", logits, f32, shape, dev),
+                                      None if bias is None else _tensor("bias", bias, f32, (E,), dev), T, E, k,
+                                      rules, _tensor("router_idx", router_idx, _int32(), (T, k), dev),
+                                      _tensor("router_w", router_w, f32, (T, k), dev),
+                                      raw(dev) if stream is None else int(stream))
+    if rc:
+        _check(rc)
+
+
+# ---- rows and weights in 16 bits ----
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _strided(name: str, t, shape, device: int) -> tuple:
+    """Pointer and row stride of a tensor of rows on the current GPU, whose
+    rows may lie apart."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}: expected the current GPU (cuda:{device})")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
+    if t.stride(1) != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the values of a row have to be neighbours, got strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _kind16(x, w, kinds) -> int:
+    kind = kinds.get(x.dtype, 0)
+    if x.dim() != 2 or w.dim() != 2 or not kind:
+        raise ValueError(f"x and w have to be 2-dimensional and bfloat16 or float16, got {x.dtype} {tuple(x.shape)}")
+    if max(x.shape[1], w.shape[0]) >> 31:
+        raise ValueError("x or w is beyond 32-bit sizes")
+    return kind
+
+
+def dense_16(x, w, *, bias=None, activation: str = "none", residual=None, y=None, y_q8_1=None, stream=None) -> None:
+    """Projection act(x w^T + bias) + residual of bfloat16 or float16 rows
+    x [T, K] by weights w [N, K] of the same type -> y [T, N] (float32,
+    bfloat16 or float16) and/or y_q8_1 (uint8 [T, N/32, 36]).  bias is float32
+    [N], residual [T, N] in float32, bfloat16 or float16 (it may be y);
+    activation is one of ACTIVATIONS.  The rows of x, residual and y may lie
+    apart (those of x by a multiple of 8 values)."""
+    _, f32, _, u8, kinds, cur, raw = _torch()
+    kind = _kind16(x, w, kinds)
+    T, K = x.shape
+    N = w.shape[0]
+    dev = _device("x", x, cur)
+    xp, xs = _strided("x", x, x.shape, dev)
+    shape = (T, N)
+    rp = yp = None
+    rk = rs = yk = ys = 0
+    if residual is not None:
+        rk = _rows("residual", residual, kinds)
+        rp, rs = _strided("residual", residual, shape, dev)
+    if y is not None:
+        yk = _rows("y", y, kinds)
+        yp, ys = _strided("y", y, shape, dev)
+    rc = lib().lat_moe_dense_16(xp, xs, _tensor("w", w, x.dtype, (N, K), dev), kind, T, N, K,
+                                None if bias is None else _tensor("bias", bias, f32, (N,), dev),
+                                _choice("activation", activation, ACTIVATIONS), rp, rk, rs, yp, yk, ys,
+                                None if y_q8_1 is None else _tensor("y_q8_1", y_q8_1, u8, (T, N // 32, 36), dev),
+                                raw(dev) if stream is None else int(stream))
+    if rc:
+        _check(rc)
+
+
+def gated_16(x, w, h, *, bias=None, activation: str = "silu", stream=None) -> None:
+    """Gate and up projections of a gated block on bfloat16 or float16 rows
+    x [T, K]: h = act(x gate^T + gate bias) * (x up^T + up bias).  w is [2F, K]
+    of x's type, the gate rows first; bias float32 [2F]; h [T, F] in float32,
+    bfloat16 or float16.  The rows of x and h may lie apart (those of x by a
+    multiple of 8 values).  dense_16 with a residual is the block's other
+    half."""
+    _, f32, _, _, kinds, cur, raw = _torch()
+    kind = _kind16(x, w, kinds)
+    T, K = x.shape
+    rows = w.shape[0]
+    if rows % 2:
+        raise ValueError(f"w: expected gate rows and as many up rows, got {rows} rows")
+    F = rows // 2
+    dev = _device("x", x, cur)
+    xp, xs = _strided("x", x, x.shape, dev)
+    hk = _rows("h", h, kinds)
+    hp, hs = _strided("h", h, (T, F), dev)
+    rc = lib().lat_moe_gated_16(xp, xs, _tensor("w", w, x.dtype, (rows, K), dev), kind, T, F, K,
+                                None if bias is None else _tensor("bias", bias, f32, (rows,), dev),
+                                _choice("activation", activation, ACTIVATIONS), hp, hk, hs,
+                                raw(dev) if stream is None else int(stream))
     if rc:
         _check(rc)
 

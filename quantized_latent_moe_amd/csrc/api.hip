@@ -251,6 +251,19 @@ FfnLayout ffn_layout(int64_t T, int32_t F) {
   return L;
 }
 
+// A 16-bit product's operands (rows: weight rows) and the rows of an array of
+// its output's shape.
+bool dense_16_ok(int64_t T, int64_t rows, int32_t K, int32_t type, int64_t x_stride, int32_t act) {
+  if (T < 0 || T >= (int64_t)1 << 31 || rows < 1 || rows > LAT_MOE_DENSE_16_MAX_N) return false;
+  if (K < 8 || K > 65536 || K % 8 || x_stride < K || x_stride > LAT_MOE_DENSE_16_MAX_STRIDE || x_stride % 8) return false;
+  if (type != LAT_MOE_BF16 && type != LAT_MOE_F16) return false;
+  if (act < LAT_MOE_ACT_NONE || act > LAT_MOE_ACT_GELU_TANH) return false;
+  return ((T + 63) / 64) * ((rows + 63) / 64) < (int64_t)1 << 31;
+}
+bool rows_ok(int32_t type, int64_t stride, int32_t N) {
+  return type_ok(type) && stride >= N && stride < (int64_t)1 << 31;
+}
+
 }  // namespace
 
 namespace latmoe {
@@ -473,6 +486,77 @@ int lat_moe_ffn_fp8_ex(const void* x_fp8, const float* x_scales, const void* gat
   return LAT_MOE_OK;
 }
 
+int lat_moe_router_topk_ex(const float* logits, const float* bias, int64_t T, int32_t E, int32_t k,
+                           const lat_moe_routing* routing, int32_t* router_idx, float* router_w, void* stream) {
+  if (!routing || T < 0 || T >= (int64_t)1 << 31 || E < 1 || E > LAT_MOE_ROUTER_MAX_E || k < 1 ||
+      k > LAT_MOE_ROUTER_MAX_K)
+    return LAT_MOE_EINVAL;
+  const lat_moe_routing o = *routing;
+  if (o.score != LAT_MOE_SCORE_SOFTMAX && o.score != LAT_MOE_SCORE_SIGMOID) return LAT_MOE_EINVAL;
+  if (o.groups < 1 || o.groups > LAT_MOE_ROUTER_MAX_GROUPS || E % o.groups || o.top_groups < 1 ||
+      o.top_groups > o.groups || k > o.top_groups * (E / o.groups))
+    return LAT_MOE_EINVAL;
+  if (o.top_groups < o.groups && o.group_score != LAT_MOE_GROUP_MAX &&
+      (o.group_score != LAT_MOE_GROUP_TOP2 || E / o.groups < 2))
+    return LAT_MOE_EINVAL;
+  if (!(o.scale >= -3.402823466e38f && o.scale <= 3.402823466e38f)) return LAT_MOE_EINVAL;  // NaN too
+  if (T == 0) return LAT_MOE_OK;
+  const void* ptrs[] = {logits, router_idx, router_w};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return LAT_MOE_EINVAL;
+  if (!aligned16(bias)) return LAT_MOE_EINVAL;  // null counts as aligned
+  int rc = check_device(nullptr);
+  if (rc != LAT_MOE_OK) return rc;
+  const RouterExArgs a{logits, bias, router_idx, router_w, T, E, k, o.groups, o.top_groups, o.scale,
+                       o.score == LAT_MOE_SCORE_SIGMOID, o.group_score == LAT_MOE_GROUP_TOP2, o.renormalise != 0};
+  if (launch_router_ex(a, static_cast<hipStream_t>(stream)) != hipSuccess) return LAT_MOE_ELAUNCH;
+  return LAT_MOE_OK;
+}
+
+int lat_moe_dense_16(const void* x, int64_t x_stride, const void* w, int32_t type, int64_t T, int32_t N, int32_t K,
+                     const float* bias, int32_t activation, const void* residual, int32_t residual_type,
+                     int64_t residual_stride, void* y, int32_t y_type, int64_t y_stride, void* y_q8_1, void* stream) {
+  if (!dense_16_ok(T, N, K, type, x_stride, activation)) return LAT_MOE_EINVAL;
+  if (residual && !rows_ok(residual_type, residual_stride, N)) return LAT_MOE_EINVAL;
+  if (y && !rows_ok(y_type, y_stride, N)) return LAT_MOE_EINVAL;
+  if (y_q8_1 && N % 32) return LAT_MOE_EINVAL;
+  if (T == 0) return LAT_MOE_OK;
+  if (!x || !w || (!y && !y_q8_1)) return LAT_MOE_EINVAL;
+  const void* ptrs[] = {x, w, bias, residual, y, y_q8_1};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return LAT_MOE_EINVAL;  // null counts as aligned
+  // in place only where an element's place stays its own
+  if (residual && residual == y && (residual_type != y_type || residual_stride != y_stride)) return LAT_MOE_EINVAL;
+  int num_cus = 1;
+  int rc = check_device(&num_cus);
+  if (rc != LAT_MOE_OK) return rc;
+  const bool vec = N % 8 == 0 && (!y || y_stride % 8 == 0) && (!residual || residual_stride % 8 == 0);
+  const Dense16Args a{x, w, T, x_stride, N, K, 0, 0,
+                      {bias, residual, y, static_cast<uint8_t*>(y_q8_1), residual_stride, y_stride, residual_type,
+                       y_type, activation, N, vec}};
+  if (launch_dense_16(a, type, false, num_cus, static_cast<hipStream_t>(stream)) != hipSuccess)
+    return LAT_MOE_ELAUNCH;
+  return LAT_MOE_OK;
+}
+
+int lat_moe_gated_16(const void* x, int64_t x_stride, const void* w, int32_t type, int64_t T, int32_t F, int32_t K,
+                     const float* bias, int32_t activation, void* h, int32_t h_type, int64_t h_stride, void* stream) {
+  if (!dense_16_ok(T, 2 * (int64_t)F, K, type, x_stride, activation)) return LAT_MOE_EINVAL;
+  if (T == 0) return LAT_MOE_OK;
+  if (!x || !w || !h || !rows_ok(h_type, h_stride, F)) return LAT_MOE_EINVAL;
+  const void* ptrs[] = {x, w, bias, h};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return LAT_MOE_EINVAL;  // null counts as aligned
+  int num_cus = 1;
+  int rc = check_device(&num_cus);
+  if (rc != LAT_MOE_OK) return rc;
+  const Dense16Args a{x, w, T, x_stride, F, K, 0, 0,
+                      {bias, nullptr, h, nullptr, 0, h_stride, 0, h_type, activation, F,
+                       F % 8 == 0 && h_stride % 8 == 0}};
+  if (launch_dense_16(a, type, true, num_cus, static_cast<hipStream_t>(stream)) != hipSuccess) return LAT_MOE_ELAUNCH;
+  return LAT_MOE_OK;
+}
+
 const char* lat_moe_strerror(int code) {
   switch (code) {
     case LAT_MOE_OK: return "ok";
@@ -485,6 +569,6 @@ const char* lat_moe_strerror(int code) {
   }
 }
 
-int lat_moe_version(void) { return 201; }
+int lat_moe_version(void) { return 202; }
 
 }  // extern "C"

@@ -234,6 +234,19 @@ bool dense_ws_shape(int N, int K);
 hipError_t launch_dense_ws(const uint8_t* x, const uint8_t* w, int wfmt, int64_t T, int N, int K, float* y_f32,
                            uint8_t* y_q8, const ProbeRows* probe, int num_cus, hipStream_t st);
 
+// Scores with a bias, groups, top-k (lat_moe_router_topk_ex).
+struct RouterExArgs {
+  const float* logits;
+  const float* bias;  // or null
+  int32_t* idx;
+  float* w;
+  int64_t T;
+  int E, k, groups, top_groups;
+  float scale;
+  bool sigmoid, top2, renormalise;
+};
+hipError_t launch_router_ex(const RouterExArgs& a, hipStream_t st);
+
 // Rows to e4m3 with a scale for each 128 values.
 hipError_t launch_quantize_fp8(const void* x, int x_type, int64_t rows, int cols, uint8_t* codes, float* scales,
                                hipStream_t st);
@@ -279,5 +292,27 @@ hipError_t launch_gateup_fp8_small(const uint8_t* x, const float* xs, const uint
 // through h32 [T][F] (not read before it is written).
 hipError_t launch_gateup_fp8(const uint8_t* x, const float* xs, const uint8_t* gu, const float* gus, int64_t T, int F,
                              int C, bool exact, float* h32, uint8_t* h, float* hs, int num_cus, hipStream_t st);
+
+// 16-bit rows [T][K] x 16-bit weights [N][K] (gated: [2N][K], gate rows then up
+// rows): the products, and what follows them.
+struct Epilogue16 {
+  const float* bias;     // [N] (gated: [2N], gate then up), or null
+  const void* residual;  // or null
+  void* y;               // or null
+  uint8_t* y_q8;         // or null
+  int64_t residual_stride, y_stride;
+  int residual_type, y_type, act;
+  int N;                 // columns of y
+  bool vec;              // rows of y and of the residual are whole pieces of 8 values
+};
+struct Dense16Args {
+  const void* x;
+  const void* w;
+  int64_t T, x_stride;
+  int N, K;         // N: columns of the output
+  int n_nt, n_tt;   // weight and token tiles
+  Epilogue16 e;
+};
+hipError_t launch_dense_16(Dense16Args a, int type, bool gated, int num_cus, hipStream_t st);
 
 }  // namespace latmoe
