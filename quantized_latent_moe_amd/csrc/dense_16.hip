@@ -1,20 +1,21 @@
-// Products of 16-bit rows with 16-bit weights: the dense projection with bias,
-// activation and residual, and the gated pair.
+// Products of 16-bit rows with 16-bit weights, for batches of whole token
+// tiles: the dense projection with bias, activation and residual, and the gated
+// pair.
 //
 //   y[t][n] = act(sum over k of x[t][k] w[n][k] + bias[n]) + residual[t][n]
 //   h[t][f] = act(gate) * up
-//
-// A workgroup of four waves takes 64 weight rows (gated: 32 gate rows and the
-// same columns' up rows) x 64 tokens, in steps of 64 values of K.
+#include <algorithm>
+
 #include "epilogue16.h"
 
 namespace latmoe {
 namespace {
 
-constexpr int kStep = 64;          // K per step
-constexpr int kRowBytes = 2 * kStep;
-
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+
+constexpr int kXcds = 8;
+constexpr int kStep = 64;              // K per step
+constexpr int kRowBytes = 2 * kStep;   // of a step's row in LDS
 
 template <int TYPE>
 __device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c) {
@@ -24,91 +25,286 @@ __device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
-template <int TYPE, bool GATED>
-__global__ __launch_bounds__(256) void k_dense_16(const Dense16Args a) {
-  __shared__ __align__(16) uint8_t As[64 * kRowBytes], Bs[64 * kRowBytes];
-  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+// A buffer's descriptor in scalar registers (raw, stride 0).
+__device__ __forceinline__ v4i descriptor(const void* base, uint32_t bytes) {
+  const uint64_t p = (uint64_t)base;
+  return v4i{(int)(uint32_t)p, (int)(uint32_t)(p >> 32) & 0xffff, (int)bytes, 0x00020000};
+}
+// Direct load into LDS: 16 bytes a lane, from voff + soff of the buffer to
+// `lds` + 16 lane (an offset past the buffer's records brings zeros).  As
+// assembly, which the compiler does not count: it would wait for every load on
+// its way before any LDS read, since it cannot tell the stages apart.  The
+// waits are those of loads_done_barrier.  No register is written.
+__device__ __forceinline__ void load_lds(v4i buffer, uint32_t lds, int voff, int soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(buffer), "s"(soff)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+__device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
+
+// Wait until at most N of this wave's accesses to memory and none of its LDS
+// accesses are outstanding, then for the workgroup.
+template <int N>
+__device__ __forceinline__ void loads_done_barrier() {
+  static_assert(N < 64, "vmcnt has 6 bits");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// Tile order: groups of kGroup weight tiles sweep the token tiles, and each
+// XCD takes a contiguous piece of that order, so that the tiles an XCD works
+// on at one time share rows in its L2.
+constexpr int kGroup = 4;
+__device__ __forceinline__ void tile_of(const Dense16Args& a, int number, int& nt, int& tt) {
+  const int items = a.n_nt * a.n_tt;
+  const int xcd = number % kXcds, idx = number / kXcds;
+  const int q = items / kXcds, r = items % kXcds;
+  const int item = xcd * q + min(xcd, r) + idx;
+  const int group = item / (kGroup * a.n_tt);
+  const int within = item - group * kGroup * a.n_tt;
+  const int g = min(kGroup, a.n_nt - group * kGroup);
+  tt = within / g;
+  nt = group * kGroup + (within - tt * g);
+}
+
+template <int TYPE, int FA, int FB, int WN, int WT, bool GATED, int STAGES>
+struct Tile {
+  static constexpr int kWaves = WN * WT, kThreads = 64 * kWaves;
+  static constexpr int TN = 16 * FA * WN, TT = 16 * FB * WT;
+  static constexpr int COLS = GATED ? TN / 2 : TN;  // columns of the output
+  static constexpr int kLoadsA = TN / 8 / kWaves, kLoadsB = TT / 8 / kWaves, kLoads = kLoadsA + kLoadsB;  // 1 KB each
+  static_assert(TN % (8 * kWaves) == 0 && TT % (8 * kWaves) == 0, "whole loads");
+  static_assert(FA % 4 == 0, "the results are transposed four fragments at a time");
+  static_assert(STAGES >= 2, "a step ahead");
+  static constexpr int kA = TN * kRowBytes, kB = TT * kRowBytes;  // bytes of a stage
+
+  // Output column (within the tile) of LDS row r of the weight tile, gated
+  // tiles: each wave's 16 FA rows are FA/2 gate fragments and the same columns'
+  // up fragments.
+  static __device__ __forceinline__ int gated_col(int r) {
+    const int wave_rows = 16 * FA;
+    return (r / wave_rows) * (wave_rows / 2) + (r % (wave_rows / 2));
+  }
+  static __device__ __forceinline__ bool gated_up(int r) { return (r % (16 * FA)) >= 8 * FA; }
+
+  struct Place {
+    int n0, n_live, t_live;
+    int64_t t0;
+  };
+  static __device__ __forceinline__ Place place(const Dense16Args& a, int number) {
+    int nt, tt;
+    tile_of(a, number, nt, tt);
+    Place p;
+    p.n0 = nt * COLS;
+    p.t0 = (int64_t)tt * TT;
+    p.n_live = min(COLS, a.N - p.n0);
+    p.t_live = (int)min((int64_t)TT, a.T - p.t0);
+    return p;
+  }
+
+  // What a wave loads: the tile's buffers (weight rows, gated: the up rows,
+  // tokens), and the lane's byte offset in each of its pieces at K step 0.
+  // Only the step's start, in the scalar offset, changes.  Rows past the
+  // tile's last, and what lies past a row's end, have an offset past the
+  // buffer's records: their loads return zeros.
+  struct Source {
+    v4i w, up, x;
+    int vw[kLoadsA], vx[kLoadsB];
+  };
+  static __device__ __forceinline__ int row_in_tile(int piece, int lane) { return 8 * piece + (lane >> 3); }
+  static __device__ __forceinline__ int chunk_in_step(int row, int lane) { return ((lane & 7) ^ swz(row)) << 4; }
+  static __device__ __forceinline__ void open(Source& src, const Dense16Args& a, const Place& at, int wave, int lane) {
+    const uint16_t* w = static_cast<const uint16_t*>(a.w);
+    const int row_w = 2 * a.K, row_x = 2 * (int)a.x_stride;
+    const uint32_t bytes_w = (uint32_t)at.n_live * row_w;
+    src.w = descriptor(w + (int64_t)at.n0 * a.K, bytes_w);
+    src.up = GATED ? descriptor(w + ((int64_t)a.N + at.n0) * a.K, bytes_w) : src.w;
+    src.x = descriptor(static_cast<const uint16_t*>(a.x) + at.t0 * a.x_stride,
+                      (uint32_t)(at.t_live - 1) * row_x + 2 * a.K);
+#pragma unroll
+    for (int j = 0; j < kLoadsA; ++j) {
+      const int r = row_in_tile(wave * kLoadsA + j, lane), row = GATED ? gated_col(r) : r;
+      src.vw[j] = row < at.n_live ? row * row_w + chunk_in_step(r, lane) : kOutOfRange;
+    }
+#pragma unroll
+    for (int j = 0; j < kLoadsB; ++j) {
+      const int r = row_in_tile(wave * kLoadsB + j, lane);
+      src.vx[j] = r < at.t_live ? r * row_x + chunk_in_step(r, lane) : kOutOfRange;
+    }
+  }
+  // Chunks at or past `end` of the coming step read as zeros, and so do all later ones.
+  static __device__ __forceinline__ void cut(Source& src, int end, int wave, int lane) {
+#pragma unroll
+    for (int j = 0; j < kLoadsA; ++j)
+      if (chunk_in_step(row_in_tile(wave * kLoadsA + j, lane), lane) >= end) src.vw[j] = kOutOfRange;
+#pragma unroll
+    for (int j = 0; j < kLoadsB; ++j)
+      if (chunk_in_step(row_in_tile(wave * kLoadsB + j, lane), lane) >= end) src.vx[j] = kOutOfRange;
+  }
+  // The wave's j-th direct load of a K step into LDS: weight rows, then tokens.
+  static __device__ __forceinline__ void load_piece(int j, const Source& src, uint32_t As, uint32_t Bs, int k0,
+                                                    int wave) {
+    if (j < kLoadsA) {
+      const int piece = wave * kLoadsA + j;  // rows 8 piece .. +7
+      load_lds(GATED && gated_up(8 * piece) ? src.up : src.w, As + piece * 1024, src.vw[j], k0);
+    } else {
+      const int piece = wave * kLoadsB + j - kLoadsA;
+      load_lds(src.x, Bs + piece * 1024, src.vx[j - kLoadsA], k0);
+    }
+  }
+
+  static __device__ __forceinline__ v4i fragment(const uint8_t* at, int i) {
+    return *reinterpret_cast<const v4i*>(at + i * 16 * kRowBytes);
+  }
+};
+
+template <int TYPE, int FA, int FB, int WN, int WT, bool GATED, int STAGES>
+__global__ __launch_bounds__(64 * WN * WT) void k_dense_16(const Dense16Args a) {
+  using D = Tile<TYPE, FA, FB, WN, WT, GATED, STAGES>;
+  __shared__ __align__(16) uint8_t As[STAGES * D::kA], Bs[STAGES * D::kB];
+  const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const uint32_t number = workgroup_number();
-  if (number >= (uint32_t)a.n_nt * (uint32_t)a.n_tt) return;
-  constexpr int COLS = GATED ? 32 : 64;
-  const int n0 = (int)(number % a.n_nt) * COLS;
-  const int64_t t0 = (int64_t)(number / a.n_nt) * 64;
-  const uint16_t* xp = static_cast<const uint16_t*>(a.x);
-  const uint16_t* wp = static_cast<const uint16_t*>(a.w);
-  v4f acc[4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += kStep) {
-    for (int p = tid; p < 64 * 8; p += 256) {
-      const int row = p >> 3, k = k0 + (p & 7) * 8;
-      uint4 va = {0, 0, 0, 0}, vb = {0, 0, 0, 0};
-      const int n = n0 + (GATED ? row & 31 : row);
-      if (n < a.N && k < a.K)
-        va = *reinterpret_cast<const uint4*>(wp + ((int64_t)n + (GATED && row >= 32 ? a.N : 0)) * a.K + k);
-      if (t0 + row < a.T && k < a.K) vb = *reinterpret_cast<const uint4*>(xp + (t0 + row) * a.x_stride + k);
-      *reinterpret_cast<uint4*>(As + row * kRowBytes + (p & 7) * 16) = va;
-      *reinterpret_cast<uint4*>(Bs + row * kRowBytes + (p & 7) * 16) = vb;
-    }
-    __syncthreads();
+  const int first = (int)workgroup_number();
+  if (first >= a.n_nt * a.n_tt) return;  // the whole workgroup
+  const int wn = wave % WN, wt = wave / WN;
+  const int steps = (a.K + kStep - 1) / kStep;
+  const int tail = a.K % kStep ? 2 * (a.K % kStep) : kRowBytes;
+  const typename D::Place at = D::place(a, first);
+  typename D::Source src;
+  D::open(src, a, at, wave, lane);
+  int step = 0;  // loaded next
+  auto prepare = [&]() {
+    const int end = step >= steps ? 0 : step == steps - 1 ? tail : kRowBytes;
+    if (end < kRowBytes) D::cut(src, end, wave, lane);
+  };
+
+  const int row = lane & 15, g = lane >> 4;
+  const int off0 = row * kRowBytes + ((g ^ swz(row)) << 4);
+  const int a_off = wn * 16 * FA * kRowBytes + off0, b_off = wt * 16 * FB * kRowBytes + off0;
+  v4i fa[FA][2], fb[FB][2];
+  v4f acc[FA][FB] = {};
+
+  const uint32_t al = lds_address(As), bl = lds_address(Bs);
+  int buf = 0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const v4i b = *reinterpret_cast<const v4i*>(Bs + (16 * wave + r) * kRowBytes + (4 * h + g) * 16);
+  for (int s = 0; s < STAGES; ++s) {
+    prepare();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const v4i w = *reinterpret_cast<const v4i*>(As + (16 * i + r) * kRowBytes + (4 * h + g) * 16);
-        acc[i] = mfma16<TYPE>(w, b, acc[i]);
+    for (int j = 0; j < D::kLoads; ++j)
+      D::load_piece(j, src, al + s * D::kA, bl + s * D::kB, step * kRowBytes, wave);
+    ++step;
+  }
+  loads_done_barrier<(STAGES - 1) * D::kLoads>();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < FA; ++i) fa[i][h] = D::fragment(As + (a_off ^ (64 * h)), i);
+#pragma unroll
+    for (int j = 0; j < FB; ++j) fb[j][h] = D::fragment(Bs + (b_off ^ (64 * h)), j);
+  }
+  constexpr int M = 2 * FA * FB;  // MFMAs of a step
+  constexpr int Q = FB;           // of which so many come before the step's barrier
+#pragma unroll 1
+  for (int s = 0; s < steps; ++s) {
+    // The step's fragments are in registers.  At its barrier the next step has
+    // landed, and every wave has read this step's buffers, which then take step
+    // s + STAGES; each fragment's registers take the next step's as soon as
+    // their last MFMA has been issued.
+    const int next = buf + 1 == STAGES ? 0 : buf + 1;
+    const uint8_t* An = As + next * D::kA;
+    const uint8_t* Bn = Bs + next * D::kB;
+    prepare();
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int h = m / (FA * FB), i = m / FB % FA, j = m % FB;
+      acc[i][j] = mfma16<TYPE>(fa[i][h], fb[j][h], acc[i][j]);
+      if (m == Q - 1) loads_done_barrier<(STAGES - 2) * D::kLoads>();
+      if (m >= Q - 1) {
+        // loads, spread over the first half of what is left
+        constexpr int kSpan = (M - Q) / 2 / D::kLoads < 1 ? 1 : (M - Q) / 2 / D::kLoads;
+        const int p = m - (Q - 1);
+        if (p % kSpan == 0 && p / kSpan < D::kLoads)
+          D::load_piece(p / kSpan, src, al + buf * D::kA, bl + buf * D::kB, step * kRowBytes, wave);
+        if (j == FB - 1) fa[i][h] = D::fragment(An + (a_off ^ (64 * h)), i);
+        if (i == FA - 1) fb[j][h] = D::fragment(Bn + (b_off ^ (64 * h)), j);
       }
+      __builtin_amdgcn_sched_barrier(0);  // the scheduler keeps this order
     }
-    __syncthreads();
+    ++step;
+    buf = next;
   }
-  // transposed among the lane groups: lane (r, g) then holds fragment g's 16 columns of token r
-  float v[16];
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no load may still write LDS when the workgroup ends
+
+  // transposed among the lane groups: lane (r, g) then holds 16 columns of fragment q + g, of one token
+  const int fr = lane & 15;
+  static_assert(kFinishPitch * 4 * D::kThreads <= STAGES * D::kA, "a part of the stages for each lane");
+  __syncthreads();  // the stages are free
+  float* lds = reinterpret_cast<float*>(As) + kFinishPitch * tid;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    uint32_t q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = __builtin_bit_cast(uint32_t, (float)acc[i][e]);
-    transpose4(q);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[4 * i + e] = __builtin_bit_cast(float, q[i]);
-  }
-  const int64_t t = t0 + 16 * wave + r;
-  float b[16];
-  if constexpr (GATED) {
-    const int n = n0 + 16 * (g & 1);
-    load_bias16(a.e.bias ? a.e.bias + (g < 2 ? 0 : a.N) : nullptr, n, a.N, b);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += b[i];
-    if (g < 2) activate<16>(v, a.e.act);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] *= __shfl_xor(v[i], 32);
-    if (g < 2 && t < a.T && n < a.N) finish16(a.e, t, n, v);
-  } else {
-    const int n = n0 + 16 * g;
-    const bool live = t < a.T && n < a.N;
+  for (int q = 0; q < (GATED ? FA / 2 : FA); q += 4) {
+    const bool have = !GATED || FA / 2 >= 4 || g < FA / 2;
+    const int c = (GATED ? wn * 8 * FA : wn * 16 * FA) + 16 * (q + g), n = at.n0 + c;
+    float b[16], bu[16];
     load_bias16(a.e.bias, n, a.N, b);
+    if (GATED) load_bias16(a.e.bias ? a.e.bias + a.N : nullptr, n, a.N, bu);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += b[i];
-    activate<16>(v, a.e.act);
-    if (live) finish16(a.e, t, n, v);
-    if (a.e.y_q8) store_q8(a.e.y_q8 + (t * (a.N / 32) + n / 32) * kQ81Bytes, v, !(g & 1), 16, live);
+    for (int j = 0; j < FB; ++j) {
+      auto gather = [&](int base, float* v) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t u[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            u[i] = __builtin_bit_cast(uint32_t, (float)acc[base + i < FA ? base + i : base][j][e]);
+          transpose4(u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[4 * i + e] = __builtin_bit_cast(float, u[i]);
+        }
+      };
+      float v[16];
+      gather(q, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] += b[i];
+      activate<16>(v, a.e.act);
+      if constexpr (GATED) {
+        float u[16];
+        gather(q + FA / 2, u);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] *= u[i] + bu[i];
+      }
+      const int tl = wt * 16 * FB + 16 * j + fr;
+      const bool live = tl < at.t_live && n < a.N && have;
+      const int64_t t = at.t0 + tl;
+      if (live) finish16(a.e, t, n, v, lds);
+      if (!GATED && a.e.y_q8) store_q8(a.e.y_q8 + (t * (a.N / 32) + n / 32) * kQ81Bytes, v, !(g & 1), 16, live);
+    }
   }
+}
+
+template <int TYPE, int FA, int FB, int WN, int WT, bool GATED, int STAGES>
+hipError_t run(Dense16Args a, hipStream_t st) {
+  using D = Tile<TYPE, FA, FB, WN, WT, GATED, STAGES>;
+  a.n_nt = (a.N + D::COLS - 1) / D::COLS;
+  a.n_tt = (int)((a.T + D::TT - 1) / D::TT);
+  const dim3 grid = grid_of((int64_t)a.n_nt * a.n_tt);
+  hipLaunchKernelGGL((k_dense_16<TYPE, FA, FB, WN, WT, GATED, STAGES>), grid, dim3(D::kThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+template <int TYPE>
+hipError_t launch(const Dense16Args& a, bool gated, int num_cus, hipStream_t st) {
+  if (gated) return run<TYPE, 8, 4, 2, 4, true, 2>(a, st);
+  return run<TYPE, 8, 4, 2, 4, false, 2>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_dense_16(Dense16Args a, int type, bool gated, int num_cus, hipStream_t st) {
-  const int cols = gated ? 32 : 64;
-  a.n_nt = (a.N + cols - 1) / cols;
-  a.n_tt = (int)((a.T + 63) / 64);
-  const dim3 grid = grid_of((int64_t)a.n_nt * a.n_tt), block(256);
-  if (type == LAT_MOE_BF16) {
-    if (gated) hipLaunchKernelGGL((k_dense_16<LAT_MOE_BF16, true>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((k_dense_16<LAT_MOE_BF16, false>), grid, block, 0, st, a);
-  } else {
-    if (gated) hipLaunchKernelGGL((k_dense_16<LAT_MOE_F16, true>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((k_dense_16<LAT_MOE_F16, false>), grid, block, 0, st, a);
-  }
-  return hipGetLastError();
+  return type == LAT_MOE_BF16 ? launch<LAT_MOE_BF16>(a, gated, num_cus, st) : launch<LAT_MOE_F16>(a, gated, num_cus, st);
 }
 
 }  // namespace latmoe

@@ -68,41 +68,62 @@ __device__ __forceinline__ void load8(const void* base, int type, int64_t elem, 
   }
 }
 
+typedef float v4f_unaligned __attribute__((ext_vector_type(4), aligned(4)));
+
 // Bias of the 16 columns from n on, a multiple of 16 (columns past `count` have none).
 __device__ __forceinline__ void load_bias16(const float* bias, int n, int count, float* b) {
-  if (bias && n + 16 <= count) {
+  const int live = bias ? count - n : 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) b[i] = bias[n + i];
-  } else {
+  for (int i = 0; i < 16; ++i) b[i] = 0.f;
+  if (live >= 16) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) b[i] = bias && n + i < count ? bias[n + i] : 0.f;
+    for (int i = 0; i < 16; i += 4) {
+      const v4f_unaligned p = *reinterpret_cast<const v4f_unaligned*>(bias + n + i);
+      b[i] = p[0];
+      b[i + 1] = p[1];
+      b[i + 2] = p[2];
+      b[i + 3] = p[3];
+    }
+  } else if (live > 0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) b[i] = i < live ? bias[n + min(i, live - 1)] : 0.f;
   }
 }
 
 // Residual and y of row t's 16 columns from n on, a multiple of 16: v is what
-// the activation left, and becomes what is rounded.  n < e.N.
-__device__ __forceinline__ void finish16(const Epilogue16& e, int64_t t, int n, float* v) {
+// the activation left, and becomes what is rounded.  n < e.N.  `lds`: 16 floats
+// of the lane's own, where rows that are not whole pieces take their values
+// from one by one (unrolled, that path would be most of a kernel's code).
+__device__ __forceinline__ void finish16(const Epilogue16& e, int64_t t, int n, float* v, float* lds) {
   if (e.vec) {
 #pragma unroll
     for (int h = 0; h < 16; h += 8) {
-      if (n + h >= e.N) break;
-      if (e.residual) {
-        float r[8];
-        load8(e.residual, e.residual_type, t * e.residual_stride + n + h, r);
+      if (n + h < e.N) {
+        if (e.residual) {
+          float r[8];
+          load8(e.residual, e.residual_type, t * e.residual_stride + n + h, r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[h + i] += r[i];
+          for (int i = 0; i < 8; ++i) v[h + i] += r[i];
+        }
+        if (e.y) store8(e.y, e.y_type, t * e.y_stride + n + h, v + h);
       }
-      if (e.y) store8(e.y, e.y_type, t * e.y_stride + n + h, v + h);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (n + i >= e.N) break;
-      if (e.residual) v[i] += load1(e.residual, e.residual_type, t * e.residual_stride + n + i);
-      if (e.y) store1(e.y, e.y_type, t * e.y_stride + n + i, v[i]);
+    for (int i = 0; i < 16; ++i) lds[i] = v[i];
+    const int live = min(16, e.N - n);
+#pragma unroll 1
+    for (int i = 0; i < live; ++i) {
+      float u = lds[i];
+      if (e.residual) u += load1(e.residual, e.residual_type, t * e.residual_stride + n + i);
+      if (e.y) store1(e.y, e.y_type, t * e.y_stride + n + i, u);
+      lds[i] = u;
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = lds[i];
   }
 }
+constexpr int kFinishPitch = 17;  // floats of a lane's part: no two lanes of a piece in one bank
 
 // q8_1 block of a row of 32 columns that two lanes hold, 16 each (`first`: the
 // block's first 16); `other` is the distance between the two lanes.
