@@ -80,7 +80,7 @@ struct Tile {
   static_assert(TN % (8 * kWaves) == 0 && TT % (8 * kWaves) == 0, "whole loads");
   static_assert(FA % 4 == 0, "the results are transposed four fragments at a time");
   static_assert(STAGES >= 2, "a step ahead");
-  static constexpr int kA = TN * kRowBytes, kB = TT * kRowBytes;  // bytes of a stage
+  static constexpr int kA = TN * kRowBytes, kStage = kA + TT * kRowBytes;  // bytes of a stage: weights, then tokens
 
   // Output column (within the tile) of LDS row r of the weight tile, gated
   // tiles: each wave's 16 FA rows are FA/2 gate fragments and the same columns'
@@ -146,14 +146,13 @@ struct Tile {
       if (chunk_in_step(row_in_tile(wave * kLoadsB + j, lane), lane) >= end) src.vx[j] = kOutOfRange;
   }
   // The wave's j-th direct load of a K step into LDS: weight rows, then tokens.
-  static __device__ __forceinline__ void load_piece(int j, const Source& src, uint32_t As, uint32_t Bs, int k0,
-                                                    int wave) {
+  static __device__ __forceinline__ void load_piece(int j, const Source& src, uint32_t stage, int k0, int wave) {
     if (j < kLoadsA) {
       const int piece = wave * kLoadsA + j;  // rows 8 piece .. +7
-      load_lds(GATED && gated_up(8 * piece) ? src.up : src.w, As + piece * 1024, src.vw[j], k0);
+      load_lds(GATED && gated_up(8 * piece) ? src.up : src.w, stage + piece * 1024, src.vw[j], k0);
     } else {
       const int piece = wave * kLoadsB + j - kLoadsA;
-      load_lds(src.x, Bs + piece * 1024, src.vx[j - kLoadsA], k0);
+      load_lds(src.x, stage + kA + piece * 1024, src.vx[j - kLoadsA], k0);
     }
   }
 
@@ -165,7 +164,7 @@ struct Tile {
 template <int TYPE, int FA, int FB, int WN, int WT, bool GATED, int STAGES>
 __global__ __launch_bounds__(64 * WN * WT) void k_dense_16(const Dense16Args a) {
   using D = Tile<TYPE, FA, FB, WN, WT, GATED, STAGES>;
-  __shared__ __align__(16) uint8_t As[STAGES * D::kA], Bs[STAGES * D::kB];
+  __shared__ __align__(16) uint8_t stages[STAGES * D::kStage];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int first = (int)workgroup_number();
@@ -184,27 +183,27 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_16(const Dense16Args a) 
 
   const int row = lane & 15, g = lane >> 4;
   const int off0 = row * kRowBytes + ((g ^ swz(row)) << 4);
-  const int a_off = wn * 16 * FA * kRowBytes + off0, b_off = wt * 16 * FB * kRowBytes + off0;
+  const int a_off = wn * 16 * FA * kRowBytes + off0, b_off = D::kA + wt * 16 * FB * kRowBytes + off0;
   v4i fa[FA][2], fb[FB][2];
   v4f acc[FA][FB] = {};
 
-  const uint32_t al = lds_address(As), bl = lds_address(Bs);
+  const uint32_t base = lds_address(stages);
   int buf = 0;
 #pragma unroll
   for (int s = 0; s < STAGES; ++s) {
     prepare();
 #pragma unroll
     for (int j = 0; j < D::kLoads; ++j)
-      D::load_piece(j, src, al + s * D::kA, bl + s * D::kB, step * kRowBytes, wave);
+      D::load_piece(j, src, base + s * D::kStage, step * kRowBytes, wave);
     ++step;
   }
   loads_done_barrier<(STAGES - 1) * D::kLoads>();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int i = 0; i < FA; ++i) fa[i][h] = D::fragment(As + (a_off ^ (64 * h)), i);
+    for (int i = 0; i < FA; ++i) fa[i][h] = D::fragment(stages + (a_off ^ (64 * h)), i);
 #pragma unroll
-    for (int j = 0; j < FB; ++j) fb[j][h] = D::fragment(Bs + (b_off ^ (64 * h)), j);
+    for (int j = 0; j < FB; ++j) fb[j][h] = D::fragment(stages + (b_off ^ (64 * h)), j);
   }
   constexpr int M = 2 * FA * FB;  // MFMAs of a step
   constexpr int Q = FB;           // of which so many come before the step's barrier
@@ -215,8 +214,7 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_16(const Dense16Args a) 
     // s + STAGES; each fragment's registers take the next step's as soon as
     // their last MFMA has been issued.
     const int next = buf + 1 == STAGES ? 0 : buf + 1;
-    const uint8_t* An = As + next * D::kA;
-    const uint8_t* Bn = Bs + next * D::kB;
+    const uint8_t* ahead = stages + next * D::kStage;
     prepare();
 #pragma unroll
     for (int m = 0; m < M; ++m) {
@@ -228,9 +226,9 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_16(const Dense16Args a) 
         constexpr int kSpan = (M - Q) / 2 / D::kLoads < 1 ? 1 : (M - Q) / 2 / D::kLoads;
         const int p = m - (Q - 1);
         if (p % kSpan == 0 && p / kSpan < D::kLoads)
-          D::load_piece(p / kSpan, src, al + buf * D::kA, bl + buf * D::kB, step * kRowBytes, wave);
-        if (j == FB - 1) fa[i][h] = D::fragment(An + (a_off ^ (64 * h)), i);
-        if (i == FA - 1) fb[j][h] = D::fragment(Bn + (b_off ^ (64 * h)), j);
+          D::load_piece(p / kSpan, src, base + buf * D::kStage, step * kRowBytes, wave);
+        if (j == FB - 1) fa[i][h] = D::fragment(ahead + (a_off ^ (64 * h)), i);
+        if (i == FA - 1) fb[j][h] = D::fragment(ahead + (b_off ^ (64 * h)), j);
       }
       __builtin_amdgcn_sched_barrier(0);  // the scheduler keeps this order
     }
@@ -239,50 +237,11 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_16(const Dense16Args a) 
   }
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no load may still write LDS when the workgroup ends
 
-  // transposed among the lane groups: lane (r, g) then holds 16 columns of fragment q + g, of one token
-  const int fr = lane & 15;
-  static_assert(kFinishPitch * 4 * D::kThreads <= STAGES * D::kA, "a part of the stages for each lane");
+  using E = TileEpilogue<FA, FB, GATED>;
+  static_assert(D::kWaves * E::kBytes <= STAGES * D::kStage, "a part of the stages for each wave");
   __syncthreads();  // the stages are free
-  float* lds = reinterpret_cast<float*>(As) + kFinishPitch * tid;
-#pragma unroll
-  for (int q = 0; q < (GATED ? FA / 2 : FA); q += 4) {
-    const bool have = !GATED || FA / 2 >= 4 || g < FA / 2;
-    const int c = (GATED ? wn * 8 * FA : wn * 16 * FA) + 16 * (q + g), n = at.n0 + c;
-    float b[16], bu[16];
-    load_bias16(a.e.bias, n, a.N, b);
-    if (GATED) load_bias16(a.e.bias ? a.e.bias + a.N : nullptr, n, a.N, bu);
-#pragma unroll
-    for (int j = 0; j < FB; ++j) {
-      auto gather = [&](int base, float* v) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t u[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            u[i] = __builtin_bit_cast(uint32_t, (float)acc[base + i < FA ? base + i : base][j][e]);
-          transpose4(u);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[4 * i + e] = __builtin_bit_cast(float, u[i]);
-        }
-      };
-      float v[16];
-      gather(q, v);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] += b[i];
-      activate<16>(v, a.e.act);
-      if constexpr (GATED) {
-        float u[16];
-        gather(q + FA / 2, u);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] *= u[i] + bu[i];
-      }
-      const int tl = wt * 16 * FB + 16 * j + fr;
-      const bool live = tl < at.t_live && n < a.N && have;
-      const int64_t t = at.t0 + tl;
-      if (live) finish16(a.e, t, n, v, lds);
-      if (!GATED && a.e.y_q8) store_q8(a.e.y_q8 + (t * (a.N / 32) + n / 32) * kQ81Bytes, v, !(g & 1), 16, live);
-    }
-  }
+  E::run(a.e, acc, reinterpret_cast<float*>(stages + wave * E::kBytes), at.n0 + wn * E::OUT, at.t0 + wt * 16 * FB,
+         at.t_live - wt * 16 * FB, lane);
 }
 
 template <int TYPE, int FA, int FB, int WN, int WT, bool GATED, int STAGES>

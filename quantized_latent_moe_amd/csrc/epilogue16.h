@@ -52,32 +52,16 @@ __device__ __forceinline__ void store1(void* base, int type, int64_t elem, float
   if (type == LAT_MOE_F32) static_cast<float*>(base)[elem] = v;
   else static_cast<uint16_t*>(base)[elem] = (uint16_t)(type == LAT_MOE_BF16 ? pack_bf16(v, v) : pack_f16(v, v));
 }
-__device__ __forceinline__ void load8(const void* base, int type, int64_t elem, float* v) {
-  if (type == LAT_MOE_F32) {
-    Raw8<LAT_MOE_F32> r;
-    r.load(base, elem);
-    r.values(v);
-  } else if (type == LAT_MOE_BF16) {
-    Raw8<LAT_MOE_BF16> r;
-    r.load(base, elem);
-    r.values(v);
-  } else {
-    Raw8<LAT_MOE_F16> r;
-    r.load(base, elem);
-    r.values(v);
-  }
-}
-
 typedef float v4f_unaligned __attribute__((ext_vector_type(4), aligned(4)));
 
-// Bias of the 16 columns from n on, a multiple of 16 (columns past `count` have none).
-__device__ __forceinline__ void load_bias16(const float* bias, int n, int count, float* b) {
+// The 8 columns from n on of a row of `count` columns (those past it: zeros).
+__device__ __forceinline__ void load_bias8(const float* bias, int n, int count, float* b) {
   const int live = bias ? count - n : 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) b[i] = 0.f;
-  if (live >= 16) {
+  for (int i = 0; i < 8; ++i) b[i] = 0.f;
+  if (live >= 8) {
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
+    for (int i = 0; i < 8; i += 4) {
       const v4f_unaligned p = *reinterpret_cast<const v4f_unaligned*>(bias + n + i);
       b[i] = p[0];
       b[i + 1] = p[1];
@@ -86,71 +70,165 @@ __device__ __forceinline__ void load_bias16(const float* bias, int n, int count,
     }
   } else if (live > 0) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) b[i] = i < live ? bias[n + min(i, live - 1)] : 0.f;
+    for (int i = 0; i < 8; ++i) b[i] = i < live ? bias[n + min(i, live - 1)] : 0.f;
   }
 }
 
-// Residual and y of row t's 16 columns from n on, a multiple of 16: v is what
-// the activation left, and becomes what is rounded.  n < e.N.  `lds`: 16 floats
-// of the lane's own, where rows that are not whole pieces take their values
-// from one by one (unrolled, that path would be most of a kernel's code).
-__device__ __forceinline__ void finish16(const Epilogue16& e, int64_t t, int n, float* v, float* lds) {
-  if (e.vec) {
+// Eight values of a type known at run time, as they lie in memory.
+struct Piece8 {
+  uint4 a, b;  // b: fp32 only
+  __device__ __forceinline__ void load(const void* base, int type, int64_t elem) {
+    if (type == LAT_MOE_F32) {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + elem);
+      a = p[0];
+      b = p[1];
+    } else {
+      a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + elem);
+    }
+  }
+  __device__ __forceinline__ void add_to(int type, float* v) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w}, u[4] = {b.x, b.y, b.z, b.w};
+    if (type == LAT_MOE_F32) {
 #pragma unroll
-    for (int h = 0; h < 16; h += 8) {
-      if (n + h < e.N) {
-        if (e.residual) {
-          float r[8];
-          load8(e.residual, e.residual_type, t * e.residual_stride + n + h, r);
+      for (int i = 0; i < 4; ++i) {
+        v[i] += __builtin_bit_cast(float, w[i]);
+        v[4 + i] += __builtin_bit_cast(float, u[i]);
+      }
+    } else if (type == LAT_MOE_BF16) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[h + i] += r[i];
-        }
-        if (e.y) store8(e.y, e.y_type, t * e.y_stride + n + h, v + h);
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] += __builtin_bit_cast(float, w[i] << 16);
+        v[2 * i + 1] += __builtin_bit_cast(float, w[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] += half_bits_to_float(w[i] & 0xffffu);
+        v[2 * i + 1] += half_bits_to_float(w[i] >> 16);
       }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) lds[i] = v[i];
-    const int live = min(16, e.N - n);
-#pragma unroll 1
-    for (int i = 0; i < live; ++i) {
-      float u = lds[i];
-      if (e.residual) u += load1(e.residual, e.residual_type, t * e.residual_stride + n + i);
-      if (e.y) store1(e.y, e.y_type, t * e.y_stride + n + i, u);
-      lds[i] = u;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = lds[i];
   }
-}
-constexpr int kFinishPitch = 17;  // floats of a lane's part: no two lanes of a piece in one bank
+};
 
-// q8_1 block of a row of 32 columns that two lanes hold, 16 each (`first`: the
-// block's first 16); `other` is the distance between the two lanes.
-__device__ __forceinline__ void store_q8(uint8_t* block, const float* v, bool first, int other, bool live) {
+// q8_1 block of a row of 32 columns that four neighbouring lanes hold, 8 each.
+__device__ __forceinline__ void store_q8(uint8_t* block, const float* v, int part, bool live) {
 #pragma clang fp contract(off)
   float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = max_or_nan(amax, fabsf(v[i]));
-  amax = max_or_nan(amax, __shfl_xor(amax, other));
+  for (int i = 0; i < 8; ++i) amax = max_or_nan(amax, fabsf(v[i]));
+  amax = max_or_nan(amax, __shfl_xor(amax, 1));
+  amax = max_or_nan(amax, __shfl_xor(amax, 2));
   const float d = amax / 127.0f;
   const float id = d != 0.0f ? 1.0f / d : 0.0f;
-  uint32_t pk[4];
+  uint32_t pk[2];
   int sum = 0;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < 2; ++q) {
     pk[q] = pack_codes(round_half_away(v[4 * q] * id), round_half_away(v[4 * q + 1] * id),
                        round_half_away(v[4 * q + 2] * id), round_half_away(v[4 * q + 3] * id));
     sum = __builtin_amdgcn_sdot4((int)pk[q], 0x01010101, sum, false);
   }
-  sum += __shfl_xor(sum, other);
+  sum += __shfl_xor(sum, 1);
+  sum += __shfl_xor(sum, 2);
   if (!live) return;
-  uint32_t* w = reinterpret_cast<uint32_t*>(block) + (first ? 1 : 5);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) w[q] = pk[q];
-  if (first)
-    *reinterpret_cast<uint32_t*>(block) =
-        float_to_half_bits(d) | (float_to_half_bits(fp32_barrier(d * (float)sum)) << 16);
+  uint32_t* w = reinterpret_cast<uint32_t*>(block);
+  w[1 + 2 * part] = pk[0];
+  w[2 + 2 * part] = pk[1];
+  if (part == 0) w[0] = float_to_half_bits(d) | (float_to_half_bits(fp32_barrier(d * (float)sum)) << 16);
 }
+
+// What follows a wave's 16 FA weight rows x 16 FB tokens of a product.  The
+// results pass through LDS, 16 tokens at a time, so that a row's columns lie in
+// neighbouring lanes (whole lines are stored, 8 columns a lane) and so that the
+// code is there once and not for each register: unrolled it took 6 us a tile to
+// fetch.  A wave uses its own part of LDS, whose accesses are in order.
+//   first  bias, activation and the gated product, where there are any
+//   then   residual and stores; the residual's loads run ahead by 16 tokens
+template <int FA, int FB, bool GATED>
+struct TileEpilogue {
+  static constexpr int OUT = GATED ? 8 * FA : 16 * FA;  // columns of the wave
+  static constexpr int kLanes = OUT / 8;                // of a row
+  static constexpr int kRows = 64 / kLanes;             // at a time
+  static constexpr int kPasses = 16 / kRows;            // of 16 tokens
+  static constexpr int kPitch = 16 * FA + 4;            // floats between rows: no two lanes of a store in one bank
+  static constexpr int kBytes = 16 * kPitch * 4;        // of LDS for a wave
+  static_assert(64 % kLanes == 0 && 16 % kRows == 0, "whole rows");
+
+  // n0: the wave's first column; t0: its first token; live: its tokens inside the matrix.
+  static __device__ __forceinline__ void run(const Epilogue16& e, const v4f (&acc)[FA][FB], float* lds, int n0,
+                                             int64_t t0, int live, int lane) {
+    const int r = lane & 15, g = lane >> 4;
+    const int c = (lane % kLanes) * 8, row = lane / kLanes, n = n0 + c;
+    const bool shape = GATED || e.bias || e.act != LAT_MOE_ACT_NONE;
+    float b[8], bu[8];
+    load_bias8(e.bias, n, e.N, b);
+    if (GATED) load_bias8(e.bias ? e.bias + e.N : nullptr, n, e.N, bu);
+    const bool inside = n < e.N, pieces = e.vec && e.residual && inside;
+    Piece8 ahead[kPasses];
+    auto fetch = [&](int j, int p) {
+      const int tl = 16 * j + kRows * p + row;
+      if (pieces && tl < live) ahead[p].load(e.residual, e.residual_type, (t0 + tl) * e.residual_stride + n);
+    };
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) fetch(0, p);
+#pragma unroll 1
+    for (int j = 0; j < FB; ++j) {
+      if (16 * j >= live) break;  // the whole wave
+#pragma unroll
+      for (int q = 0; q < FB; ++q)
+        if (q == j) {
+#pragma unroll
+          for (int i = 0; i < FA; ++i) *reinterpret_cast<v4f*>(lds + r * kPitch + 16 * i + 4 * g) = acc[i][q];
+        }
+      if (shape) {
+#pragma unroll 1
+        for (int p = 0; p < kPasses; ++p) {
+          v4f* at = reinterpret_cast<v4f*>(lds + (kRows * p + row) * kPitch + c);
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = at[i / 4][i % 4] + b[i];
+          activate<8>(v, e.act);
+          if constexpr (GATED) {
+            const v4f* up = reinterpret_cast<const v4f*>(lds + (kRows * p + row) * kPitch + OUT + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= up[i / 4][i % 4] + bu[i];
+          }
+          at[0] = v4f{v[0], v[1], v[2], v[3]};
+          at[1] = v4f{v[4], v[5], v[6], v[7]};
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int tl = 16 * j + kRows * p + row;
+        const int64_t t = t0 + tl;
+        const bool stored = inside && tl < live;
+        float* at = lds + (kRows * p + row) * kPitch + c;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = reinterpret_cast<v4f*>(at)[i / 4][i % 4];
+        if (stored) {
+          if (e.vec) {
+            if (e.residual) ahead[p].add_to(e.residual_type, v);
+            if (e.y) store8(e.y, e.y_type, t * e.y_stride + n, v);
+          } else {
+            const int count = min(8, e.N - n);
+#pragma unroll 1
+            for (int i = 0; i < count; ++i) {
+              float u = at[i];
+              if (e.residual) u += load1(e.residual, e.residual_type, t * e.residual_stride + n + i);
+              if (e.y) store1(e.y, e.y_type, t * e.y_stride + n + i, u);
+              at[i] = u;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = reinterpret_cast<v4f*>(at)[i / 4][i % 4];
+          }
+        }
+        if (j + 1 < FB) fetch(j + 1, p);
+        if (!GATED && e.y_q8)
+          store_q8(e.y_q8 + (t * (e.N / 32) + n / 32) * kQ81Bytes, v, lane & 3, stored);
+      }
+    }
+  }
+};
 
 }  // namespace latmoe
