@@ -1,0 +1,54 @@
+// Choice of the tile of a 16-bit product: host code without any GPU header, so
+// that it can be compiled and looked at by itself.
+#pragma once
+
+#include <stdint.h>
+
+namespace latmoe {
+
+// Large tiles move fewer bytes for a product, small ones fill the chip with few
+// rows and leave less of its last pass idle.  The time of a variant is
+// estimated from what a K step of 64 was measured to take (us): on every CU at
+// once, each with all the tiles that it holds, and with one tile a CU on part of
+// the chip; and from what a tile costs beside its steps.
+struct Dense16Tile {
+  int rows, tokens;  // weight rows (gated: half of them gate rows) and tokens
+  int per_cu;        // tiles a CU holds (LDS)
+  float full, alone, tile;
+  int64_t count(int64_t T, int64_t weight_rows) const {
+    return (T + tokens - 1) / tokens * ((weight_rows + rows - 1) / rows);
+  }
+};
+
+constexpr Dense16Tile kDense16Tiles[] = {
+    // 21000 x 4096 by 4096 | 5268 x 4096 by 1024 | 517 x 2056 by 4104 | 512 x 4096 by 4096 (us):
+    {256, 256, 1, 1.45f, 1.13f, 5.f},  // 597 | 77 | 55 | 73
+    {256, 192, 1, 1.27f, 0.92f, 5.f},  // 611 | 64 | 47 | 62
+    {256, 128, 1, 0.87f, 0.66f, 4.f},  // 630 | 53 | 35 | 45
+    {128, 128, 1, 0.51f, 0.42f, 3.f},  // 783 | 60 | 24 | 30
+    {128, 128, 2, 0.96f, 0.60f, 4.f},  // 697 | 53 | 28 | 39: the same with fewer stages, two on a CU
+    {128, 64, 2, 0.66f, 0.28f, 4.f},   // 920 | 60 | 31 | 22
+    {64, 64, 2, 0.37f, 0.21f, 3.f},    // 1024 | 71 | 29 | 28
+};
+constexpr int kDense16Variants = 7;
+
+// The variant with the least estimated time; steps: of K; weight_rows: gated
+// ones counted twice.
+inline int dense16_pick_tile(int64_t T, int64_t weight_rows, int steps, int num_cus) {
+  int best = 0;
+  float least = 0.f;
+  for (int i = 0; i < kDense16Variants; ++i) {
+    const Dense16Tile& v = kDense16Tiles[i];
+    const int64_t tiles = v.count(T, weight_rows), slots = (int64_t)num_cus * v.per_cu;
+    const int64_t passes = tiles / slots, rest = tiles % slots;
+    float t = (float)passes * (v.full * (float)steps + v.tile);
+    if (rest) t += (rest <= num_cus ? v.alone : v.full) * (float)steps + v.tile;
+    if (i == 0 || t < least) {
+      best = i;
+      least = t;
+    }
+  }
+  return best;
+}
+
+}  // namespace latmoe

@@ -6,6 +6,7 @@
 //   h[t][f] = act(gate) * up
 #include <algorithm>
 
+#include "dense16_tiles.h"
 #include "epilogue16.h"
 
 namespace latmoe {
@@ -78,7 +79,7 @@ struct Tile {
   static constexpr int COLS = GATED ? TN / 2 : TN;  // columns of the output
   static constexpr int kLoadsA = TN / 8 / kWaves, kLoadsB = TT / 8 / kWaves, kLoads = kLoadsA + kLoadsB;  // 1 KB each
   static_assert(TN % (8 * kWaves) == 0 && TT % (8 * kWaves) == 0, "whole loads");
-  static_assert(FA % 4 == 0, "the results are transposed four fragments at a time");
+  static_assert(!GATED || FA % 2 == 0, "as many gate fragments as up fragments");
   static_assert(STAGES >= 2, "a step ahead");
   static constexpr int kA = TN * kRowBytes, kStage = kA + TT * kRowBytes;  // bytes of a stage: weights, then tokens
 
@@ -244,9 +245,12 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_16(const Dense16Args a) 
          at.t_live - wt * 16 * FB, lane);
 }
 
-template <int TYPE, int FA, int FB, int WN, int WT, bool GATED, int STAGES>
+// V: the variant's place in the table.
+template <int V, int TYPE, int FA, int FB, int WN, int WT, bool GATED, int STAGES>
 hipError_t run(Dense16Args a, hipStream_t st) {
   using D = Tile<TYPE, FA, FB, WN, WT, GATED, STAGES>;
+  static_assert(kDense16Tiles[V].rows == D::TN && kDense16Tiles[V].tokens == D::TT, "the tile that the choice knows");
+  static_assert(kDense16Tiles[V].per_cu * STAGES * D::kStage <= 160 * 1024, "LDS of a CU");
   a.n_nt = (a.N + D::COLS - 1) / D::COLS;
   a.n_tt = (int)((a.T + D::TT - 1) / D::TT);
   const dim3 grid = grid_of((int64_t)a.n_nt * a.n_tt);
@@ -254,16 +258,25 @@ hipError_t run(Dense16Args a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int TYPE>
-hipError_t launch(const Dense16Args& a, bool gated, int num_cus, hipStream_t st) {
-  if (gated) return run<TYPE, 8, 4, 2, 4, true, 2>(a, st);
-  return run<TYPE, 8, 4, 2, 4, false, 2>(a, st);
+template <int TYPE, bool GATED>
+hipError_t launch(const Dense16Args& a, int num_cus, hipStream_t st) {
+  switch (dense16_pick_tile(a.T, (GATED ? 2 : 1) * (int64_t)a.N, (a.K + kStep - 1) / kStep, num_cus)) {
+    case 0: return run<0, TYPE, 8, 4, 2, 4, GATED, 2>(a, st);
+    case 1: return run<1, TYPE, 8, 3, 2, 4, GATED, 2>(a, st);
+    case 2: return run<2, TYPE, 8, 2, 2, 4, GATED, 3>(a, st);
+    case 3: return run<3, TYPE, 4, 2, 2, 4, GATED, 4>(a, st);
+    case 4: return run<4, TYPE, 4, 2, 2, 4, GATED, 2>(a, st);
+    case 5: return run<5, TYPE, 4, 1, 2, 4, GATED, 3>(a, st);
+    default: return run<6, TYPE, 4, 1, 1, 4, GATED, 4>(a, st);
+  }
 }
 
 }  // namespace
 
-hipError_t launch_dense_16(Dense16Args a, int type, bool gated, int num_cus, hipStream_t st) {
-  return type == LAT_MOE_BF16 ? launch<LAT_MOE_BF16>(a, gated, num_cus, st) : launch<LAT_MOE_F16>(a, gated, num_cus, st);
+hipError_t launch_dense_16(const Dense16Args& a, int type, bool gated, int num_cus, hipStream_t st) {
+  if (type == LAT_MOE_BF16)
+    return gated ? launch<LAT_MOE_BF16, true>(a, num_cus, st) : launch<LAT_MOE_BF16, false>(a, num_cus, st);
+  return gated ? launch<LAT_MOE_F16, true>(a, num_cus, st) : launch<LAT_MOE_F16, false>(a, num_cus, st);
 }
 
 }  // namespace latmoe
