@@ -28,9 +28,10 @@ constexpr Dense16Tile kDense16Tiles[] = {
     {128, 128, 1, 0.51f, 0.42f, 3.f},  // 783 | 60 | 24 | 30
     {128, 128, 2, 0.96f, 0.60f, 4.f},  // 697 | 53 | 28 | 39: the same with fewer stages, two on a CU
     {128, 64, 2, 0.66f, 0.28f, 4.f},   // 920 | 60 | 31 | 22
-    {64, 64, 2, 0.37f, 0.21f, 3.f},    // 1024 | 71 | 29 | 28
+    {64, 64, 2, 0.37f, 0.21f, 3.f},    // 1024 | 71 | 29 | 29
+    {64, 32, 1, 0.145f, 0.12f, 3.f},   // K dealt to four slices of waves; 512 x 4096 by 1024 12.6 (64 x 64: 15)
 };
-constexpr int kDense16Variants = 7;
+constexpr int kDense16Variants = 8;
 
 // The variant with the least estimated time; steps: of K; weight_rows: gated
 // ones counted twice.
@@ -49,6 +50,21 @@ inline int dense16_pick_tile(int64_t T, int64_t weight_rows, int steps, int num_
     }
   }
   return best;
+}
+
+// The kernel that streams the weights takes 4, 8 or 16 of them to a workgroup
+// (gated at least 8) and 4, 8 or 16 tokens.  It beats the tiles as long as each
+// workgroup has a CU (us here | in tiles, K = 4096): 16 x 4096 6.9 | 13, 64 x 1024 6.1 | 10.1, 512 x 128 6.8 | 10.2; with two
+// on a CU no longer: 128 x 1024 10.4 | 10.1, 64 x 4096 22 | 12.5.
+inline bool dense16_small(int64_t T, int64_t weight_rows, int num_cus) {
+  return T <= 16 || (T + 15) / 16 * ((weight_rows + 15) / 16) <= num_cus;
+}
+// As few rows as leave a workgroup for each CU.
+inline int dense16_small_rows(int64_t T, int64_t weight_rows, int num_cus) {
+  const int64_t groups = (T + 15) / 16;
+  if (weight_rows * groups <= 4 * (int64_t)num_cus) return 4;
+  if (weight_rows * groups <= 8 * (int64_t)num_cus || T <= 8) return 8;
+  return 16;
 }
 
 }  // namespace latmoe

@@ -12,19 +12,10 @@
 namespace latmoe {
 namespace {
 
-typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 constexpr int kXcds = 8;
 constexpr int kStep = 64;              // K per step
 constexpr int kRowBytes = 2 * kStep;   // of a step's row in LDS
-
-template <int TYPE>
-__device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c) {
-  if constexpr (TYPE == LAT_MOE_BF16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
-}
 
 // A buffer's descriptor in scalar registers (raw, stride 0).
 __device__ __forceinline__ v4i descriptor(const void* base, uint32_t bytes) {
@@ -72,9 +63,9 @@ __device__ __forceinline__ void tile_of(const Dense16Args& a, int number, int& n
   nt = group * kGroup + (within - tt * g);
 }
 
-template <int TYPE, int FA, int FB, int WN, int WT, bool GATED, int STAGES>
+template <int TYPE, int FA, int FB, int WN, int WT, int WK, bool GATED, int STAGES>
 struct Tile {
-  static constexpr int kWaves = WN * WT, kThreads = 64 * kWaves;
+  static constexpr int kWaves = WN * WT, kThreads = 64 * kWaves * WK;  // waves of a slice of K
   static constexpr int TN = 16 * FA * WN, TT = 16 * FB * WT;
   static constexpr int COLS = GATED ? TN / 2 : TN;  // columns of the output
   static constexpr int kLoadsA = TN / 8 / kWaves, kLoadsB = TT / 8 / kWaves, kLoads = kLoadsA + kLoadsB;  // 1 KB each
@@ -162,12 +153,13 @@ struct Tile {
   }
 };
 
-template <int TYPE, int FA, int FB, int WN, int WT, bool GATED, int STAGES>
-__global__ __launch_bounds__(64 * WN * WT) void k_dense_16(const Dense16Args a) {
-  using D = Tile<TYPE, FA, FB, WN, WT, GATED, STAGES>;
-  __shared__ __align__(16) uint8_t stages[STAGES * D::kStage];
+template <int TYPE, int FA, int FB, int WN, int WT, int WK, bool GATED, int STAGES>
+__global__ __launch_bounds__(64 * WN * WT * WK) void k_dense_16(const Dense16Args a) {
+  using D = Tile<TYPE, FA, FB, WN, WT, WK, GATED, STAGES>;
+  __shared__ __align__(16) uint8_t stages[WK * STAGES * D::kStage];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % D::kWaves;
+  const int wk = __builtin_amdgcn_readfirstlane(tid >> 6) / D::kWaves;
   const int first = (int)workgroup_number();
   if (first >= a.n_nt * a.n_tt) return;  // the whole workgroup
   const int wn = wave % WN, wt = wave / WN;
@@ -176,7 +168,7 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_16(const Dense16Args a) 
   const typename D::Place at = D::place(a, first);
   typename D::Source src;
   D::open(src, a, at, wave, lane);
-  int step = 0;  // loaded next
+  int step = wk;  // loaded next
   auto prepare = [&]() {
     const int end = step >= steps ? 0 : step == steps - 1 ? tail : kRowBytes;
     if (end < kRowBytes) D::cut(src, end, wave, lane);
@@ -188,7 +180,8 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_16(const Dense16Args a) 
   v4i fa[FA][2], fb[FB][2];
   v4f acc[FA][FB] = {};
 
-  const uint32_t base = lds_address(stages);
+  uint8_t* const own = stages + wk * STAGES * D::kStage;  // the slice's stages
+  const uint32_t base = lds_address(own);
   int buf = 0;
 #pragma unroll
   for (int s = 0; s < STAGES; ++s) {
@@ -196,26 +189,26 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_16(const Dense16Args a) 
 #pragma unroll
     for (int j = 0; j < D::kLoads; ++j)
       D::load_piece(j, src, base + s * D::kStage, step * kRowBytes, wave);
-    ++step;
+    step += WK;
   }
   loads_done_barrier<(STAGES - 1) * D::kLoads>();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int i = 0; i < FA; ++i) fa[i][h] = D::fragment(stages + (a_off ^ (64 * h)), i);
+    for (int i = 0; i < FA; ++i) fa[i][h] = D::fragment(own + (a_off ^ (64 * h)), i);
 #pragma unroll
-    for (int j = 0; j < FB; ++j) fb[j][h] = D::fragment(stages + (b_off ^ (64 * h)), j);
+    for (int j = 0; j < FB; ++j) fb[j][h] = D::fragment(own + (b_off ^ (64 * h)), j);
   }
   constexpr int M = 2 * FA * FB;  // MFMAs of a step
   constexpr int Q = FB;           // of which so many come before the step's barrier
 #pragma unroll 1
-  for (int s = 0; s < steps; ++s) {
+  for (int s = 0; s < steps; s += WK) {
     // The step's fragments are in registers.  At its barrier the next step has
     // landed, and every wave has read this step's buffers, which then take step
     // s + STAGES; each fragment's registers take the next step's as soon as
     // their last MFMA has been issued.
     const int next = buf + 1 == STAGES ? 0 : buf + 1;
-    const uint8_t* ahead = stages + next * D::kStage;
+    const uint8_t* ahead = own + next * D::kStage;
     prepare();
 #pragma unroll
     for (int m = 0; m < M; ++m) {
@@ -233,47 +226,72 @@ __global__ __launch_bounds__(64 * WN * WT) void k_dense_16(const Dense16Args a) 
       }
       __builtin_amdgcn_sched_barrier(0);  // the scheduler keeps this order
     }
-    ++step;
+    step += WK;
     buf = next;
   }
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no load may still write LDS when the workgroup ends
 
   using E = TileEpilogue<FA, FB, GATED>;
-  static_assert(D::kWaves * E::kBytes <= STAGES * D::kStage, "a part of the stages for each wave");
+  static_assert(D::kWaves * E::kBytes <= WK * STAGES * D::kStage, "a part of the stages for each wave");
   __syncthreads();  // the stages are free
+  if constexpr (WK > 1) {
+    // the slices' sums, added in their order by the first slice's waves
+    static_assert((WK - 1) * D::kWaves * FA * FB * 1024 <= WK * STAGES * D::kStage, "a part of the stages for each wave");
+    v4f* sums = reinterpret_cast<v4f*>(stages) + wave * FA * FB * 64 + lane;
+    constexpr int kSlice = D::kWaves * FA * FB * 64;
+    if (wk > 0) {
+#pragma unroll
+      for (int i = 0; i < FA; ++i)
+#pragma unroll
+        for (int j = 0; j < FB; ++j) sums[(wk - 1) * kSlice + (i * FB + j) * 64] = acc[i][j];
+    }
+    __syncthreads();
+    if (wk == 0) {
+#pragma unroll
+      for (int q = 0; q < WK - 1; ++q)
+#pragma unroll
+        for (int i = 0; i < FA; ++i)
+#pragma unroll
+          for (int j = 0; j < FB; ++j) acc[i][j] += sums[q * kSlice + (i * FB + j) * 64];
+    }
+    __syncthreads();  // the epilogue takes other parts
+    if (wk > 0) return;
+  }
   E::run(a.e, acc, reinterpret_cast<float*>(stages + wave * E::kBytes), at.n0 + wn * E::OUT, at.t0 + wt * 16 * FB,
          at.t_live - wt * 16 * FB, lane);
 }
 
 // V: the variant's place in the table.
-template <int V, int TYPE, int FA, int FB, int WN, int WT, bool GATED, int STAGES>
+template <int V, int TYPE, int FA, int FB, int WN, int WT, int WK, bool GATED, int STAGES>
 hipError_t run(Dense16Args a, hipStream_t st) {
-  using D = Tile<TYPE, FA, FB, WN, WT, GATED, STAGES>;
+  using D = Tile<TYPE, FA, FB, WN, WT, WK, GATED, STAGES>;
   static_assert(kDense16Tiles[V].rows == D::TN && kDense16Tiles[V].tokens == D::TT, "the tile that the choice knows");
-  static_assert(kDense16Tiles[V].per_cu * STAGES * D::kStage <= 160 * 1024, "LDS of a CU");
+  static_assert(kDense16Tiles[V].per_cu * WK * STAGES * D::kStage <= 160 * 1024, "LDS of a CU");
   a.n_nt = (a.N + D::COLS - 1) / D::COLS;
   a.n_tt = (int)((a.T + D::TT - 1) / D::TT);
   const dim3 grid = grid_of((int64_t)a.n_nt * a.n_tt);
-  hipLaunchKernelGGL((k_dense_16<TYPE, FA, FB, WN, WT, GATED, STAGES>), grid, dim3(D::kThreads), 0, st, a);
+  hipLaunchKernelGGL((k_dense_16<TYPE, FA, FB, WN, WT, WK, GATED, STAGES>), grid, dim3(D::kThreads), 0, st, a);
   return hipGetLastError();
 }
 
 template <int TYPE, bool GATED>
 hipError_t launch(const Dense16Args& a, int num_cus, hipStream_t st) {
   switch (dense16_pick_tile(a.T, (GATED ? 2 : 1) * (int64_t)a.N, (a.K + kStep - 1) / kStep, num_cus)) {
-    case 0: return run<0, TYPE, 8, 4, 2, 4, GATED, 2>(a, st);
-    case 1: return run<1, TYPE, 8, 3, 2, 4, GATED, 2>(a, st);
-    case 2: return run<2, TYPE, 8, 2, 2, 4, GATED, 3>(a, st);
-    case 3: return run<3, TYPE, 4, 2, 2, 4, GATED, 4>(a, st);
-    case 4: return run<4, TYPE, 4, 2, 2, 4, GATED, 2>(a, st);
-    case 5: return run<5, TYPE, 4, 1, 2, 4, GATED, 3>(a, st);
-    default: return run<6, TYPE, 4, 1, 1, 4, GATED, 4>(a, st);
+    case 0: return run<0, TYPE, 8, 4, 2, 4, 1, GATED, 2>(a, st);
+    case 1: return run<1, TYPE, 8, 3, 2, 4, 1, GATED, 2>(a, st);
+    case 2: return run<2, TYPE, 8, 2, 2, 4, 1, GATED, 3>(a, st);
+    case 3: return run<3, TYPE, 4, 2, 2, 4, 1, GATED, 4>(a, st);
+    case 4: return run<4, TYPE, 4, 2, 2, 4, 1, GATED, 2>(a, st);
+    case 5: return run<5, TYPE, 4, 1, 2, 4, 1, GATED, 3>(a, st);
+    case 6: return run<6, TYPE, 4, 1, 1, 4, 1, GATED, 4>(a, st);
+    default: return run<7, TYPE, 4, 1, 1, 2, 4, GATED, 3>(a, st);
   }
 }
 
 }  // namespace
 
 hipError_t launch_dense_16(const Dense16Args& a, int type, bool gated, int num_cus, hipStream_t st) {
+  if (dense16_small(a.T, (gated ? 2 : 1) * (int64_t)a.N, num_cus)) return launch_dense_16_small(a, type, gated, num_cus, st);
   if (type == LAT_MOE_BF16)
     return gated ? launch<LAT_MOE_BF16, true>(a, num_cus, st) : launch<LAT_MOE_BF16, false>(a, num_cus, st);
   return gated ? launch<LAT_MOE_F16, true>(a, num_cus, st) : launch<LAT_MOE_F16, false>(a, num_cus, st);

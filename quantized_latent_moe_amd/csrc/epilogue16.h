@@ -1,10 +1,21 @@
-// What follows a 16-bit product in registers: bias, activation, residual, and
+// The 16-bit products' MFMA, and what follows a product in registers: bias, activation, residual, and
 // the stores of y and of its q8_1 blocks.
 #pragma once
 
 #include "block_fp8.h"
 
 namespace latmoe {
+
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+
+template <int TYPE>
+__device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c) {
+  if constexpr (TYPE == LAT_MOE_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+
 
 // erfc by Abramowitz and Stegun's 7.1.26: with t = 1 / (1 + p x), x >= 0,
 // (a1 t + ... + a5 t^5) exp(-x^2) is within 1.5e-7 of it, so that the

@@ -313,6 +313,8 @@ struct Dense16Args {
   int n_nt, n_tt;   // weight and token tiles
   Epilogue16 e;
 };
+// The same for few tokens or few results, by a kernel that streams the weights.
+hipError_t launch_dense_16_small(const Dense16Args& a, int type, bool gated, int num_cus, hipStream_t st);
 hipError_t launch_dense_16(const Dense16Args& a, int type, bool gated, int num_cus, hipStream_t st);
 
 }  // namespace latmoe
