@@ -23,12 +23,44 @@
 // permutes), and the owning lane marks its entry taken.  Lane j keeps pick
 // j; the k exponentials are summed across the wave and every lane divides by
 // lane 0's sum.
-#include "topk.h"
+#include "lat_moe_internal.h"
 
 namespace latmoe {
 namespace {
 
 constexpr int kRouterWaves = 4;  // tokens per workgroup
+
+// (value, index) of the better of two candidates: larger value, then lower index.
+__device__ __forceinline__ void better(float& v, int& i, float ov, int oi) {
+  if (ov > v || (ov == v && oi < i)) {
+    v = ov;
+    i = oi;
+  }
+}
+
+// One DPP step of the wave reduction: combine with the lane the control word
+// selects (rows outside row_mask keep their own pair).
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ void dpp_step(float& v, int& i) {
+  const int vb = __builtin_bit_cast(int, v);
+  const float ov = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(vb, vb, CTRL, ROW_MASK, 0xF, false));
+  const int oi = __builtin_amdgcn_update_dpp(i, i, CTRL, ROW_MASK, 0xF, false);
+  better(v, i, ov, oi);
+}
+
+// Wave-wide best (value, index), returned to every lane: DPP within the VALU
+// (quad swaps, half-row and row mirrors, row broadcasts 15 and 31) leaves the
+// result in lane 63, read back as a scalar.
+__device__ __forceinline__ void wave_best(float& v, int& i) {
+  dpp_step<0xB1, 0xF>(v, i);   // quad_perm [1,0,3,2]
+  dpp_step<0x4E, 0xF>(v, i);   // quad_perm [2,3,0,1]
+  dpp_step<0x141, 0xF>(v, i);  // row_half_mirror
+  dpp_step<0x140, 0xF>(v, i);  // row_mirror
+  dpp_step<0x142, 0xA>(v, i);  // row_bcast:15 into rows 1 and 3
+  dpp_step<0x143, 0xC>(v, i);  // row_bcast:31 into rows 2 and 3
+  v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+  i = __builtin_amdgcn_readlane(i, 63);
+}
 
 // P: logits per lane (E <= 64 P).
 template <int P>

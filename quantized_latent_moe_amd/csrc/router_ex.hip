@@ -8,7 +8,6 @@
 // 256 scores a few neighbours lie within an fp32 rounding of each other, and a
 // pick would depend on how exp rounds.
 #include "block_fp8.h"
-#include "topk.h"
 
 namespace latmoe {
 namespace {
@@ -16,25 +15,66 @@ namespace {
 constexpr int kWaves = 4;
 constexpr float kLowest = -3.402823466e38f;
 
-// exp(x), |x| <= 700, within 2^-51: x = n ln 2 + r, and the polynomial of degree
-// 10 through exp at the Chebyshev points of |r| <= ln 2 / 2 (the library's exp
-// takes twice the operations, for its last bit and its ends).
-__device__ __forceinline__ double exp64(double x) {
-  const double n = __builtin_rint(x * 0x1.71547652b82fep+0);
-  const double r = __builtin_fma(n, -0x1.62e42fefa39efp-1, x);
-  double p = 2.7626357241447223e-07;
-  p = __builtin_fma(p, r, 2.764018079620985e-06);
-  p = __builtin_fma(p, r, 2.4801504346997686e-05);
-  p = __builtin_fma(p, r, 0.00019841170270440067);
-  p = __builtin_fma(p, r, 0.0013888888932488599);
-  p = __builtin_fma(p, r, 0.008333333385667782);
-  p = __builtin_fma(p, r, 0.04166666666657314);
-  p = __builtin_fma(p, r, 0.16666666666554406);
-  p = __builtin_fma(p, r, 0.5000000000000006);
-  p = __builtin_fma(p, r, 1.0000000000000067);
-  p = __builtin_fma(p, r, 1.0);
-  return __builtin_amdgcn_ldexp(p, (int)n);
+// Across each row of 16 lanes, in all of them (quad swaps, half-row and row
+// mirrors; every lane has a source, so that the step is part of the operation).
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
 }
+__device__ __forceinline__ int row_max(int v) {
+  v = max(v, dpp<0xB1>(v));
+  v = max(v, dpp<0x4E>(v));
+  v = max(v, dpp<0x141>(v));
+  return max(v, dpp<0x140>(v));
+}
+__device__ __forceinline__ int row_min(int v) {
+  v = min(v, dpp<0xB1>(v));
+  v = min(v, dpp<0x4E>(v));
+  v = min(v, dpp<0x141>(v));
+  return min(v, dpp<0x140>(v));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_add(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)dpp<CTRL>((int)(uint32_t)b), hi = (uint32_t)dpp<CTRL>((int)(uint32_t)(b >> 32));
+  return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double row_sum(double v) {
+  return dpp_add<0x140>(dpp_add<0x141>(dpp_add<0x4E>(dpp_add<0xB1>(v))));
+}
+
+// Whole numbers in the order of the floats (no NaN, no -0), and back.
+__device__ __forceinline__ int ordered(float f) {
+  const int b = __builtin_bit_cast(int, f);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int k) {
+  return __builtin_bit_cast(float, k ^ ((k >> 31) & 0x7fffffff));
+}
+
+// exp(x), |x| <= 700, within 2^-51: x = n ln 2 + r, and the polynomial of degree
+// 10 through exp at the Chebyshev points of |r| <= ln 2 / 2.  The coefficients
+// are kept in scalar registers, which a multiply-add can read; as constants the
+// compiler moves each of them, twice 32 bits, before each use.
+struct Exp64 {
+  double c[10];
+  __device__ __forceinline__ Exp64()
+      : c{2.7626357241447223e-07, 2.764018079620985e-06, 2.4801504346997686e-05, 0.00019841170270440067,
+          0.0013888888932488599,  0.008333333385667782,  0.04166666666657314,    0.16666666666554406,
+          0.5000000000000006,     1.0000000000000067} {
+#pragma unroll
+    for (int i = 0; i < 10; ++i) asm("" : "+s"(c[i]));
+  }
+  __device__ __forceinline__ double operator()(double x) const {
+    const double n = __builtin_rint(x * 0x1.71547652b82fep+0);
+    const double r = __builtin_fma(n, -0x1.62e42fefa39efp-1, x);
+    double p = __builtin_fma(c[0], r, c[1]);
+#pragma unroll
+    for (int i = 2; i < 10; ++i) p = __builtin_fma(p, r, c[i]);
+    p = __builtin_fma(p, r, 1.0);
+    return __builtin_amdgcn_ldexp(p, (int)n);
+  }
+};
 // 1 / d, 0 < d <= e^700: the hardware's estimate (at least 20 bits) and two steps that double them.
 __device__ __forceinline__ double inverse64(double d) {
   double q = __builtin_amdgcn_rcp(d);
@@ -46,23 +86,39 @@ __device__ __forceinline__ double inverse64(double d) {
 // A logit as it counts: the largest finite number for +inf, -inf for NaN.
 __device__ __forceinline__ float counted(float l) { return l > -INFINITY ? fminf(l, -kLowest) : -INFINITY; }
 
-// What is left of the score once the row's statistics are known: exp(l - top)
-// and 1 / sum for the softmax, l and 1 for the sigmoid.  Beyond |x| = 700 a
-// score is 0 or 1 in fp32.
-__device__ __forceinline__ double unscaled(float l, float top, bool sigmoid) {
-  if (l == -INFINITY) return 0.0;
-  if (sigmoid) return inverse64(1.0 + exp64(fmin(fmax(-(double)l, -700.0), 700.0)));
-  return exp64(fmax((double)l - (double)top, -700.0));
+// What is left of the score once the row's statistics are known: exp(l - top),
+// to be divided by the row's sum, for the softmax, the score itself for the
+// sigmoid.  Beyond |x| = 700 both are 0 or 1 in fp32, for -inf too.
+__device__ __forceinline__ double sigmoid64(const Exp64& e, float l) {
+  return inverse64(1.0 + e((double)__builtin_amdgcn_fmed3f(-l, -700.0f, 700.0f)));
+}
+__device__ __forceinline__ double softmax64(const Exp64& e, float l, float top) {
+  return e(fmax((double)l - (double)top, -700.0));
 }
 
-// Candidate of a score; closed experts have the lowest.
-__device__ __forceinline__ float candidate(float l, float s, float bias) {
-  const bool open = l > -INFINITY && bias > -INFINITY;
-  return open ? fmaxf(fminf(s + bias, -kLowest), kLowest) : kLowest;
+// Candidate of a score as an ordered whole number; closed experts have the
+// lowest finite one: -inf enters the sum and is cut.
+__device__ __forceinline__ int candidate(float l, float s, float bias) {
+  const float b = bias > -INFINITY ? bias : -INFINITY;  // NaN: closed
+  return ordered(__builtin_amdgcn_fmed3f(s + (l > -INFINITY ? b : -INFINITY), kLowest, -kLowest));
+}
+// Below every candidate: an expert that cannot be picked.
+constexpr int kNone = (int)0x80000000u;
+// The fp32 sum of a group's two largest; a closed second counts as 0.
+__device__ __forceinline__ int group_score(int m1, int m2, int lowest, bool top2) {
+  return top2 && m2 > lowest ? ordered(unordered(m1) + unordered(m2)) : m1;
 }
 
 // What the other lanes of the wave have written to LDS is read after this.
 __device__ __forceinline__ void wave_lds() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
+// Weight of a pick: its score once more (a lane for each pick).
+__device__ __forceinline__ double picked(const RouterExArgs& a, const Exp64& e, const float* row, int pick, float top,
+                                         double scale) {
+  const float l = counted(row[pick]), b = a.bias ? a.bias[pick] : 0.f;
+  const float s = (float)((a.sigmoid ? sigmoid64(e, l) : softmax64(e, l, top)) * scale);
+  return l > -INFINITY && b > -INFINITY ? (double)s : 0.0;
+}
 
 // Up to 256 experts, 16 picks and 16 groups: a row of 16 lanes takes a token,
 // four tokens a wave.  Lane l holds experts 64 j + 4 l .. + 3 for each of Q
@@ -74,23 +130,23 @@ __device__ __forceinline__ void wave_lds() { __builtin_amdgcn_fence(__ATOMIC_ACQ
 // its lane takes it out of its quad.
 template <int Q>
 __global__ __launch_bounds__(64 * kWaves) void k_router_ex16(const RouterExArgs a) {
-  __shared__ __align__(16) float lds[kWaves][4][64 * Q];
-  __shared__ __align__(16) float group_lds[kWaves][4][16];
+  __shared__ __align__(16) int lds[kWaves][4][64 * Q];
+  __shared__ __align__(16) int group_lds[kWaves][4][16];
   const int lane = threadIdx.x & 63, l = lane & 15, wave = threadIdx.x >> 6;
   const int64_t t = ((int64_t)workgroup_number() * kWaves + wave) * 4 + (lane >> 4);
-  if (__builtin_amdgcn_ballot_w64(t < a.T) == 0) return;  // whole waves; a wave uses its own LDS alone
   const bool live = t < a.T;
+  if (__builtin_amdgcn_ballot_w64(live) == 0) return;  // whole waves; a wave uses its own LDS alone
   const float* row = a.logits + (live ? t : a.T - 1) * a.E;
-  float* c = lds[wave][lane >> 4];
+  int* c = lds[wave][lane >> 4] + 4 * l;
   const int E = a.E;
-  const bool fours = E % 4 == 0;
+  const Exp64 exp64;
 
   float x[Q][4], bias[Q][4];
+  if (E % 4 == 0) {
 #pragma unroll
-  for (int j = 0; j < Q; ++j) {
-    const int e = 64 * j + 4 * l;
-    if (fours) {
-      v4f v = {0.f, 0.f, 0.f, 0.f}, b = v;
+    for (int j = 0; j < Q; ++j) {
+      const int e = 64 * j + 4 * l;
+      v4f v = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, b = {0.f, 0.f, 0.f, 0.f};
       if (e < E) {
         v = *reinterpret_cast<const v4f*>(row + e);
         if (a.bias) b = *reinterpret_cast<const v4f*>(a.bias + e);
@@ -100,57 +156,66 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_ex16(const RouterExArgs 
         x[j][i] = v[i];
         bias[j][i] = b[i];
       }
-    } else {
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < Q; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[j][i] = e + i < E ? row[e + i] : 0.f;
-        bias[j][i] = a.bias && e + i < E ? a.bias[e + i] : 0.f;
+        const int e = 64 * j + 4 * l + i;
+        x[j][i] = e < E ? row[e] : -INFINITY;
+        bias[j][i] = a.bias && e < E ? a.bias[e] : 0.f;
       }
-    }
   }
-  float top = kLowest;
-  double scale = 1.0;
 #pragma unroll
   for (int j = 0; j < Q; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[j][i] = 64 * j + 4 * l + i < E ? counted(x[j][i]) : -INFINITY;
-      top = fmaxf(top, x[j][i]);
-    }
-  float quad[Q];
-  auto place = [&](int j, const double* p) {
-    float m = -INFINITY;
-    v4f v;
+    for (int i = 0; i < 4; ++i) x[j][i] = counted(x[j][i]);
+  const int lowest = ordered(kLowest);
+  float top = kLowest;
+  double scale = 1.0;
+  int quad[Q];
+  auto place = [&](int j, const float* s) {
+    v4i v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = 64 * j + 4 * l + i < E ? candidate(x[j][i], (float)(p[i] * scale), bias[j][i]) : -INFINITY;
-      m = fmaxf(m, v[i]);
+    for (int i = 0; i < 4; ++i) v[i] = candidate(x[j][i], s[i], bias[j][i]);
+    if (64 * Q > E) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = 64 * j + 4 * l + i < E ? v[i] : kNone;
     }
-    *reinterpret_cast<v4f*>(c + 64 * j + 4 * l) = v;
-    quad[j] = m;
+    *reinterpret_cast<v4i*>(c + 64 * j) = v;
+    quad[j] = max(max(v[0], v[1]), max(v[2], v[3]));
   };
   if (a.sigmoid) {
 #pragma unroll
     for (int j = 0; j < Q; ++j) {
-      double p[4];
+      float s[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = unscaled(x[j][i], 0.f, true);
-      place(j, p);
+      for (int i = 0; i < 4; ++i) s[i] = (float)sigmoid64(exp64, x[j][i]);
+      place(j, s);
     }
   } else {
-    top = row_max(top);
+#pragma unroll
+    for (int j = 0; j < Q; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, x[j][i]);
+    top = unordered(row_max(ordered(top)));
     double p[Q][4], sum = 0.0;
 #pragma unroll
     for (int j = 0; j < Q; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        p[j][i] = unscaled(x[j][i], top, false);
+        p[j][i] = softmax64(exp64, x[j][i], top);
         sum += p[j][i];
       }
-    sum = row_sum(sum);
-    scale = sum > 0.0 ? inverse64(sum) : 0.0;
+    scale = inverse64(row_sum(sum));
 #pragma unroll
-    for (int j = 0; j < Q; ++j) place(j, p[j]);
+    for (int j = 0; j < Q; ++j) {
+      float s[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = (float)(p[j][i] * scale);
+      place(j, s);
+    }
   }
   wave_lds();
 
@@ -159,77 +224,80 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_ex16(const RouterExArgs 
     const int G = a.groups, size = E / G;
     const int share = G > 8 ? 1 : G > 4 ? 2 : G > 2 ? 4 : 8;
     const int g = l / share;
-    float m1 = -INFINITY, m2 = -INFINITY;
-    if (g < G)
-      for (int i = l % share; i < size; i += share) {
-        const float v = c[g * size + i];
-        m2 = fmaxf(m2, fminf(m1, v));
-        m1 = fmaxf(m1, v);
-      }
-    auto merge = [&](float o1, float o2) {
-      m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
-      m1 = fmaxf(m1, o1);
+    int m1 = kNone, m2 = kNone;
+    auto merge = [&](int o1, int o2) {
+      m2 = max(min(m1, o1), max(m2, o2));
+      m1 = max(m1, o1);
     };
-    if (share > 1) merge(__shfl_xor(m1, 1), __shfl_xor(m2, 1));
-    if (share > 2) merge(__shfl_xor(m1, 2), __shfl_xor(m2, 2));
-    if (share > 4) merge(__shfl_xor(m1, 4), __shfl_xor(m2, 4));
-    const float score = a.top2 ? m1 + (m2 > kLowest ? m2 : 0.f) : m1;
-    float* gs = group_lds[wave][lane >> 4];
+    if (g < G) {
+      const int* member = lds[wave][lane >> 4] + g * size;
+#pragma unroll 4
+      for (int i = l % share; i < size; i += share) {
+        const int v = member[i];
+        m2 = max(m2, min(m1, v));
+        m1 = max(m1, v);
+      }
+    }
+    if (share > 1) merge(dpp<0xB1>(m1), dpp<0xB1>(m2));
+    if (share > 2) merge(dpp<0x4E>(m1), dpp<0x4E>(m2));
+    if (share > 4) merge(dpp<0x141>(m1), dpp<0x141>(m2));
+    const int score = group_score(m1, m2, lowest, a.top2);
+    int* gs = group_lds[wave][lane >> 4];
     if (l % share == 0 && g < G) gs[g] = score;
     wave_lds();
     int better = 0;
+#pragma unroll 4
     for (int q = 0; q < G; ++q) {
-      const float v = gs[q];
+      const int v = gs[q];
       better += v > score || (v == score && q < g);
     }
     // bit share * g of the row's sixteen: whether group g is kept
     const uint64_t all = __builtin_amdgcn_ballot_w64(better < a.top_groups);
     const uint32_t kept = (uint32_t)(all >> (lane & 48)) & 0xffffu;
-    const float inverse = 1.0f / (float)size;  // (e + 1/2) / size is never near a whole number
+    const float inverse = 1.0f / (float)size;
+    // (e + 1/2) / size is never near a whole number
+    auto is_kept = [&](int e) { return (kept >> ((int)(((float)e + 0.5f) * inverse) * share) & 1u) != 0; };
 #pragma unroll
     for (int j = 0; j < Q; ++j) {
       const int e = 64 * j + 4 * l;
-      v4f v = *reinterpret_cast<const v4f*>(c + e);
-      float m = -INFINITY;
+      v4i v = *reinterpret_cast<const v4i*>(c + 64 * j);
+      if (size % 4 == 0) {  // a quad lies in one group
+        if (!is_kept(e)) v = v4i{kNone, kNone, kNone, kNone};
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int of = (int)(((float)(e + i) + 0.5f) * inverse);
-        v[i] = kept >> (of * share) & 1u ? v[i] : -INFINITY;
-        m = fmaxf(m, v[i]);
+        for (int i = 0; i < 4; ++i) v[i] = is_kept(e + i) ? v[i] : kNone;
       }
-      *reinterpret_cast<v4f*>(c + e) = v;
-      quad[j] = m;
+      *reinterpret_cast<v4i*>(c + 64 * j) = v;
+      quad[j] = max(max(v[0], v[1]), max(v[2], v[3]));
     }
     wave_lds();
   }
 
   int pick = 0;
   for (int r = 0; r < a.k; ++r) {
-    float best = quad[0];
+    int best = quad[0];
 #pragma unroll
-    for (int j = 1; j < Q; ++j) best = fmaxf(best, quad[j]);
-    const float most = row_max(best);
-    int e = 4 * l;  // the lane's first quad that holds its best
+    for (int j = 1; j < Q; ++j) best = max(best, quad[j]);
+    const int most = row_max(best);
+    int at = 0;  // the lane's first quad that holds its best
 #pragma unroll
-    for (int j = Q - 1; j >= 0; --j) e = quad[j] == best ? 64 * j + 4 * l : e;
-    const v4f v = *reinterpret_cast<const v4f*>(c + e);
+    for (int j = Q - 1; j > 0; --j) at = quad[j] == best ? 64 * j : at;
+    at = quad[0] == best ? 0 : at;
+    const v4i v = *reinterpret_cast<const v4i*>(c + at);
     const int i = v[0] == best ? 0 : v[1] == best ? 1 : v[2] == best ? 2 : 3;
-    const int id = row_min(best == most ? e + i : 0x7fffffff);
-    if (id == e + i) {
-      c[id] = -INFINITY;
-      const float m = fmaxf(fmaxf(i == 0 ? -INFINITY : v[0], i == 1 ? -INFINITY : v[1]),
-                            fmaxf(i == 2 ? -INFINITY : v[2], i == 3 ? -INFINITY : v[3]));
+    const int e = at + 4 * l + i;
+    const int id = row_min(best == most ? e : 0x7fffffff);
+    if (id == e) {
+      c[at + i] = kNone;
+      const int m = max(max(i == 0 ? kNone : v[0], i == 1 ? kNone : v[1]),
+                        max(i == 2 ? kNone : v[2], i == 3 ? kNone : v[3]));
 #pragma unroll
-      for (int j = 0; j < Q; ++j) quad[j] = e >> 6 == j ? m : quad[j];
+      for (int j = 0; j < Q; ++j) quad[j] = at == 64 * j ? m : quad[j];
     }
-    if (l == r) pick = id;
+    pick = l == r ? id : pick;
   }
-  // the picks' scores once more, a lane for each
   const bool mine = l < a.k;
-  const float xl = mine ? counted(row[pick]) : -INFINITY;
-  const float xb = a.bias && mine ? a.bias[pick] : 0.f;
-  const float s = (float)(unscaled(xl, top, a.sigmoid) * scale);
-  double w = xb > -INFINITY ? (double)s : 0.0;
+  double w = mine ? picked(a, exp64, row, pick, top, scale) : 0.0;
   if (a.renormalise) {
     const double total = row_sum(w);
     w = total > 0.0 ? w / total : 0.0;
@@ -244,12 +312,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_ex16(const RouterExArgs 
 // for each group.  P: experts a lane (E <= 64 P).
 template <int P>
 __global__ __launch_bounds__(64 * kWaves) void k_router_ex(const RouterExArgs a) {
-  __shared__ float lds[kWaves][64 * P];
+  __shared__ int lds[kWaves][64 * P];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = (int64_t)workgroup_number() * kWaves + wave;
   if (t >= a.T) return;  // whole waves; a wave uses its own part of LDS alone
   const float* row = a.logits + t * a.E;
-  float x[P], c[P];
+  const Exp64 exp64;
+  float x[P];
+  int c[P];
   float top = kLowest;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
@@ -263,64 +333,66 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_ex(const RouterExArgs a)
   if (!a.sigmoid) {
     double sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < P; ++i) sum += unscaled(x[i], top, false);
+    for (int i = 0; i < P; ++i) sum += softmax64(exp64, x[i], top);
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
-    scale = sum > 0.0 ? inverse64(sum) : 0.0;
+    scale = inverse64(sum);
   }
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const int e = lane + 64 * i;
     const float b = a.bias && e < a.E ? a.bias[e] : 0.f;
-    c[i] = e < a.E ? candidate(x[i], (float)(unscaled(x[i], top, a.sigmoid) * scale), b) : -INFINITY;
+    const double p = a.sigmoid ? sigmoid64(exp64, x[i]) : softmax64(exp64, x[i], top);
+    c[i] = e < a.E ? candidate(x[i], (float)(p * scale), b) : kNone;
     lds[wave][e] = c[i];
   }
   wave_lds();
   if (a.top_groups < a.groups) {
     const int size = a.E / a.groups;
-    float score = -INFINITY;
+    int score = kNone;
     if (lane < a.groups) {
-      float m1 = -INFINITY, m2 = -INFINITY;
+      int m1 = kNone, m2 = kNone;
       for (int i = 0; i < size; ++i) {
-        const float v = lds[wave][lane * size + i];
-        m2 = fmaxf(m2, fminf(m1, v));
-        m1 = fmaxf(m1, v);
+        const int v = lds[wave][lane * size + i];
+        m2 = max(m2, min(m1, v));
+        m1 = max(m1, v);
       }
-      score = a.top2 ? m1 + (m2 > kLowest ? m2 : 0.f) : m1;
+      score = group_score(m1, m2, ordered(kLowest), a.top2);
     }
     int better = 0;
     for (int g = 0; g < a.groups; ++g) {
-      const float v = __shfl(score, g);
+      const int v = __shfl(score, g);
       better += v > score || (v == score && g < lane);
     }
-    const uint64_t kept = __ballot(lane < a.groups && better < a.top_groups);
+    const uint64_t kept = __builtin_amdgcn_ballot_w64(lane < a.groups && better < a.top_groups);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int e = lane + 64 * i;
-      if (e < a.E && !((kept >> (e / size)) & 1)) c[i] = -INFINITY;
+      if (e < a.E && !((kept >> (e / size)) & 1)) c[i] = kNone;
     }
   }
   int pick = 0;
   for (int j = 0; j < a.k; ++j) {
-    float bv = -INFINITY;
-    int bi = 0x7fffffff;
+    int bv = kNone, bi = 0x7fffffff;
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (c[i] > bv) {
         bv = c[i];
         bi = lane + 64 * i;
       }
-    wave_best(bv, bi);
+    // the wave's largest, then the lowest id that has it
+    int most = row_max(bv);
+    most = max(most, __shfl_xor(most, 16));
+    most = max(most, __shfl_xor(most, 32));
+    int id = row_min(bv == most ? bi : 0x7fffffff);
+    id = min(id, __shfl_xor(id, 16));
+    id = min(id, __shfl_xor(id, 32));
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (lane + 64 * i == bi) c[i] = -INFINITY;
-    if (lane == j) pick = bi;
+    for (int i = 0; i < P; ++i) c[i] = lane + 64 * i == id ? kNone : c[i];
+    pick = lane == j ? id : pick;
   }
   const bool mine = lane < a.k;
-  const float xl = mine ? counted(row[pick]) : -INFINITY;
-  const float xb = a.bias && mine ? a.bias[pick] : 0.f;
-  const float s = (float)(unscaled(xl, top, a.sigmoid) * scale);
-  double w = xb > -INFINITY ? (double)s : 0.0, total = w;
+  double w = mine ? picked(a, exp64, row, pick, top, scale) : 0.0, total = w;
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) total += __shfl_xor(total, m);
   if (a.renormalise) w = total > 0.0 ? w / total : 0.0;
