@@ -113,10 +113,11 @@ __device__ __forceinline__ int group_score(int m1, int m2, int lowest, bool top2
 __device__ __forceinline__ void wave_lds() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 // Weight of a pick: its score once more (a lane for each pick).
+template <bool SIGMOID>
 __device__ __forceinline__ double picked(const RouterExArgs& a, const Exp64& e, const float* row, int pick, float top,
                                          double scale) {
   const float l = counted(row[pick]), b = a.bias ? a.bias[pick] : 0.f;
-  const float s = (float)((a.sigmoid ? sigmoid64(e, l) : softmax64(e, l, top)) * scale);
+  const float s = (float)(SIGMOID ? sigmoid64(e, l) : softmax64(e, l, top) * scale);
   return l > -INFINITY && b > -INFINITY ? (double)s : 0.0;
 }
 
@@ -128,7 +129,7 @@ __device__ __forceinline__ double picked(const RouterExArgs& a, const Exp64& e, 
 // quad maximum comes by four DPP steps, each lane that holds it looks for the
 // member in its quad, the lowest id among them is picked (four more steps), and
 // its lane takes it out of its quad.
-template <int Q>
+template <int Q, bool SIGMOID>
 __global__ __launch_bounds__(64 * kWaves) void k_router_ex16(const RouterExArgs a) {
   __shared__ __align__(16) int lds[kWaves][4][64 * Q];
   __shared__ __align__(16) int group_lds[kWaves][4][16];
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_ex16(const RouterExArgs 
     *reinterpret_cast<v4i*>(c + 64 * j) = v;
     quad[j] = max(max(v[0], v[1]), max(v[2], v[3]));
   };
-  if (a.sigmoid) {
+  if constexpr (SIGMOID) {
 #pragma unroll
     for (int j = 0; j < Q; ++j) {
       float s[4];
@@ -297,7 +298,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_ex16(const RouterExArgs 
     pick = l == r ? id : pick;
   }
   const bool mine = l < a.k;
-  double w = mine ? picked(a, exp64, row, pick, top, scale) : 0.0;
+  double w = mine ? picked<SIGMOID>(a, exp64, row, pick, top, scale) : 0.0;
   if (a.renormalise) {
     const double total = row_sum(w);
     w = total > 0.0 ? w / total : 0.0;
@@ -392,7 +393,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_ex(const RouterExArgs a)
     pick = lane == j ? id : pick;
   }
   const bool mine = lane < a.k;
-  double w = mine ? picked(a, exp64, row, pick, top, scale) : 0.0, total = w;
+  double w = 0.0;
+  if (mine) w = a.sigmoid ? picked<true>(a, exp64, row, pick, top, scale) : picked<false>(a, exp64, row, pick, top, scale);
+  double total = w;
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) total += __shfl_xor(total, m);
   if (a.renormalise) w = total > 0.0 ? w / total : 0.0;
@@ -409,10 +412,11 @@ hipError_t launch_router_ex(const RouterExArgs& a, hipStream_t st) {
   const bool groups = a.top_groups < a.groups;
   if (a.E <= 256 && a.k <= 16 && (!groups || a.groups <= 16)) {
     const dim3 grid = grid_of((a.T + 4 * kWaves - 1) / (4 * kWaves));
-    if (a.E <= 64) hipLaunchKernelGGL(k_router_ex16<1>, grid, block, 0, st, a);
-    else if (a.E <= 128) hipLaunchKernelGGL(k_router_ex16<2>, grid, block, 0, st, a);
-    else if (a.E <= 192) hipLaunchKernelGGL(k_router_ex16<3>, grid, block, 0, st, a);
-    else hipLaunchKernelGGL(k_router_ex16<4>, grid, block, 0, st, a);
+    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, a); };
+    if (a.E <= 64) run(a.sigmoid ? k_router_ex16<1, true> : k_router_ex16<1, false>);
+    else if (a.E <= 128) run(a.sigmoid ? k_router_ex16<2, true> : k_router_ex16<2, false>);
+    else if (a.E <= 192) run(a.sigmoid ? k_router_ex16<3, true> : k_router_ex16<3, false>);
+    else run(a.sigmoid ? k_router_ex16<4, true> : k_router_ex16<4, false>);
     return hipGetLastError();
   }
   const dim3 grid = grid_of((a.T + kWaves - 1) / kWaves);
