@@ -287,18 +287,22 @@ FP8_BLOCK = 128
 
 
 _TORCH = None
+_INT32 = None
 
 
 def _torch():
     """What the calls below use of torch (imported on first use, as everywhere
     in this module): element types, the type codes of rows, and the current
     device's index and its current stream's handle."""
-    global _TORCH
+    global _TORCH, _INT32
     if _TORCH is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # about 0.1 us, a Stream object about 3
+        # the GPU is in use where a tensor on it is at hand: no need to look whether it is, as torch.cuda does
+        cur = getattr(torch._C, "_cuda_getDevice", None)
+        _INT32 = torch.int32
         _TORCH = (torch.float8_e4m3fn, torch.float32, torch.bfloat16, torch.uint8,
-                  {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}, torch.cuda.current_device,
+                  {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}, cur or torch.cuda.current_device,
                   raw or (lambda device: torch.cuda.current_stream(device).cuda_stream))
     return _TORCH
 
@@ -475,11 +479,6 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 GROUP_SCORES = {"max": 0, "top2": 1}
 
 
-def _int32():
-    import torch
-    return torch.int32
-
-
 def _choice(name: str, value, choices) -> int:
     code = choices.get(value)
     if code is None:
@@ -498,18 +497,21 @@ def router_topk_ex(logits, k: int, router_idx, router_w, *, bias=None, score: st
     the sum of its two largest ("top2"); weights divided by their sum if
     renormalise, and multiplied by scale.  Logits or biases of -inf close an
     expert."""
-    _, f32, _, _, _, cur, raw = _torch()
-    if logits.dim() != 2:
+    _, f32, _, _, _, cur, raw = _TORCH or _torch()
+    shape = logits.shape
+    if len(shape) != 2:
         raise ValueError("logits have to be 2-dimensional")
-    T, E = shape = logits.shape
-    dev = _device("logits", logits, cur)
+    T, E = shape
+    dev = logits.get_device()
+    if dev < 0 or dev != cur():
+        raise ValueError(f"logits are on {logits.device}: expected the current GPU")
     if max(E, k, groups, top_groups or 0) >> 31:
         raise ValueError("sizes beyond 32 bits")
     rules = Routing(_choice("score", score, SCORES), groups, groups if top_groups is None else top_groups,
                     _choice("group_score", group_score, GROUP_SCORES), renormalise, scale)
-    rc = lib().lat_moe_router_topk_ex(_tensor("logits", logits, f32, shape, dev),
+    rc = (_lib or lib()).lat_moe_router_topk_ex(_tensor("logits", logits, f32, shape, dev),
                                       None if bias is None else _tensor("bias", bias, f32, (E,), dev), T, E, k,
-                                      rules, _tensor("router_idx", router_idx, _int32(), (T, k), dev),
+                                      rules, _tensor("router_idx", router_idx, _INT32, (T, k), dev),
                                       _tensor("router_w", router_w, f32, (T, k), dev),
                                       raw(dev) if stream is None else int(stream))
     if rc:
@@ -521,27 +523,44 @@ def router_topk_ex(logits, k: int, router_idx, router_w, *, bias=None, score: st
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 
-def _strided(name: str, t, shape, device: int) -> tuple:
-    """Pointer and row stride of a tensor of rows on the current GPU, whose
-    rows may lie apart."""
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+def _strided(name: str, t, kinds, shape, device: int) -> tuple:
+    """Pointer, type code and row stride of a tensor of rows on the current
+    GPU, whose rows may lie apart."""
+    kind = kinds.get(t.dtype)
+    if kind is not None and t.shape == shape and t.get_device() == device:
+        if t.is_contiguous():
+            return t.data_ptr(), kind, shape[1]
+        if t.stride(1) == 1 or shape[1] == 1:
+            return t.data_ptr(), kind, t.stride(0) if shape[0] > 1 else shape[1]
+        raise ValueError(f"{name}: the values of a row have to be neighbours, got strides {t.stride()}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}: expected the current GPU (cuda:{device})")
-    if t.is_contiguous():
-        return t.data_ptr(), shape[1]
-    if t.stride(1) != 1 and shape[1] > 1:
-        raise ValueError(f"{name}: the values of a row have to be neighbours, got strides {t.stride()}")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+    raise ValueError(f"{name}: expected a float32, bfloat16 or float16 tensor of shape {tuple(shape)}, got {t.dtype} "
+                     f"{tuple(t.shape)}")
 
 
-def _kind16(x, w, kinds) -> int:
-    kind = kinds.get(x.dtype, 0)
-    if x.dim() != 2 or w.dim() != 2 or not kind:
-        raise ValueError(f"x and w have to be 2-dimensional and bfloat16 or float16, got {x.dtype} {tuple(x.shape)}")
-    if max(x.shape[1], w.shape[0]) >> 31:
+def _operands(x, w) -> tuple:
+    """What a 16-bit product needs to know of its operands: the current GPU,
+    x's pointer, row stride and type code, w's pointer, T, N and K."""
+    kinds, cur = (_TORCH or _torch())[4:6]
+    kind, shape, shape_w = kinds.get(x.dtype), x.shape, w.shape
+    if not kind or len(shape) != 2 or len(shape_w) != 2:
+        raise ValueError(f"x and w have to be 2-dimensional and bfloat16 or float16, got {x.dtype} {tuple(shape)} and "
+                         f"{tuple(shape_w)}")
+    T, K = shape
+    N = shape_w[0]
+    if (K | N) >> 31:
         raise ValueError("x or w is beyond 32-bit sizes")
-    return kind
+    dev = x.get_device()
+    if dev < 0 or dev != cur():
+        raise ValueError(f"x is on {x.device}: expected the current GPU")
+    if x.is_contiguous():
+        stride = K
+    elif x.stride(1) == 1 or K == 1:
+        stride = x.stride(0) if T > 1 else K
+    else:
+        raise ValueError(f"x: the values of a row have to be neighbours, got strides {x.stride()}")
+    return dev, x.data_ptr(), stride, kind, _tensor("w", w, x.dtype, (N, K), dev), T, N, K
 
 
 def dense_16(x, w, *, bias=None, activation: str = "none", residual=None, y=None, y_q8_1=None, stream=None) -> None:
@@ -551,26 +570,20 @@ def dense_16(x, w, *, bias=None, activation: str = "none", residual=None, y=None
     [N], residual [T, N] in float32, bfloat16 or float16 (it may be y);
     activation is one of ACTIVATIONS.  The rows of x, residual and y may lie
     apart (those of x by a multiple of 8 values)."""
-    _, f32, _, u8, kinds, cur, raw = _torch()
-    kind = _kind16(x, w, kinds)
-    T, K = x.shape
-    N = w.shape[0]
-    dev = _device("x", x, cur)
-    xp, xs = _strided("x", x, x.shape, dev)
-    shape = (T, N)
-    rp = yp = None
+    dev, xp, xs, kind, wp, T, N, K = _operands(x, w)
+    _, f32, _, u8, kinds, _, raw = _TORCH
+    rp = yp = qp = bp = None
     rk = rs = yk = ys = 0
     if residual is not None:
-        rk = _rows("residual", residual, kinds)
-        rp, rs = _strided("residual", residual, shape, dev)
+        rp, rk, rs = _strided("residual", residual, kinds, (T, N), dev)
     if y is not None:
-        yk = _rows("y", y, kinds)
-        yp, ys = _strided("y", y, shape, dev)
-    rc = lib().lat_moe_dense_16(xp, xs, _tensor("w", w, x.dtype, (N, K), dev), kind, T, N, K,
-                                None if bias is None else _tensor("bias", bias, f32, (N,), dev),
-                                _choice("activation", activation, ACTIVATIONS), rp, rk, rs, yp, yk, ys,
-                                None if y_q8_1 is None else _tensor("y_q8_1", y_q8_1, u8, (T, N // 32, 36), dev),
-                                raw(dev) if stream is None else int(stream))
+        yp, yk, ys = _strided("y", y, kinds, (T, N), dev)
+    if y_q8_1 is not None:
+        qp = _tensor("y_q8_1", y_q8_1, u8, (T, N // 32, 36), dev)
+    if bias is not None:
+        bp = _tensor("bias", bias, f32, (N,), dev)
+    rc = (_lib or lib()).lat_moe_dense_16(xp, xs, wp, kind, T, N, K, bp, _choice("activation", activation, ACTIVATIONS),
+                                          rp, rk, rs, yp, yk, ys, qp, raw(dev) if stream is None else int(stream))
     if rc:
         _check(rc)
 
@@ -582,21 +595,15 @@ def gated_16(x, w, h, *, bias=None, activation: str = "silu", stream=None) -> No
     bfloat16 or float16.  The rows of x and h may lie apart (those of x by a
     multiple of 8 values).  dense_16 with a residual is the block's other
     half."""
-    _, f32, _, _, kinds, cur, raw = _torch()
-    kind = _kind16(x, w, kinds)
-    T, K = x.shape
-    rows = w.shape[0]
+    dev, xp, xs, kind, wp, T, rows, K = _operands(x, w)
+    _, f32, _, _, kinds, _, raw = _TORCH
     if rows % 2:
         raise ValueError(f"w: expected gate rows and as many up rows, got {rows} rows")
     F = rows // 2
-    dev = _device("x", x, cur)
-    xp, xs = _strided("x", x, x.shape, dev)
-    hk = _rows("h", h, kinds)
-    hp, hs = _strided("h", h, (T, F), dev)
-    rc = lib().lat_moe_gated_16(xp, xs, _tensor("w", w, x.dtype, (rows, K), dev), kind, T, F, K,
-                                None if bias is None else _tensor("bias", bias, f32, (rows,), dev),
-                                _choice("activation", activation, ACTIVATIONS), hp, hk, hs,
-                                raw(dev) if stream is None else int(stream))
+    hp, hk, hs = _strided("h", h, kinds, (T, F), dev)
+    bp = None if bias is None else _tensor("bias", bias, f32, (rows,), dev)
+    rc = (_lib or lib()).lat_moe_gated_16(xp, xs, wp, kind, T, F, K, bp, _choice("activation", activation, ACTIVATIONS),
+                                          hp, hk, hs, raw(dev) if stream is None else int(stream))
     if rc:
         _check(rc)
 

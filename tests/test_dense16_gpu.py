@@ -255,3 +255,21 @@ def test_two_streams_and_a_graph():
         busy.mul_(1.0001)
         torch.cuda.synchronize()
         assert same()
+
+
+def test_binding_refuses_what_the_call_does_not_say():
+    x, w, y = torch.zeros(4, 64, device="cuda").half(), torch.zeros(96, 64, device="cuda").half(), torch.zeros(4, 96, device="cuda")
+    for call, what in ((lambda: lm.gated_16(x, w[:95], y), "gate rows"), (lambda: lm.gated_16(x, w, y), "shape"),
+                       (lambda: lm.dense_16(x, w.bfloat16(), y=y), "w: expected"), (lambda: lm.dense_16(x, w.t(), y=y), "w: expected"),
+                       (lambda: lm.dense_16(x, w, y=y[:3]), "shape"), (lambda: lm.dense_16(x, w, y=y.double()), "float32"),
+                       (lambda: lm.dense_16(x, w, y=y.t().contiguous().t()), "neighbours"),
+                       (lambda: lm.dense_16(x.t().contiguous().t(), w, y=y), "neighbours"),
+                       (lambda: lm.dense_16(x, w, y=y, bias=torch.zeros(95, device="cuda")), "bias"),
+                       (lambda: lm.dense_16(x, w, y=y, residual=y.cpu()), "current GPU"),
+                       (lambda: lm.dense_16(x, w, y=y, activation="swish"), "activation")):
+        with pytest.raises(ValueError, match=what):
+            call()
+    with pytest.raises(lm.LatMoeError):  # nothing to write
+        lm.dense_16(x, w)
+    with pytest.raises(lm.LatMoeError):  # rows of x that do not begin at a multiple of 16 bytes
+        lm.dense_16(torch.zeros(4, 68, device="cuda").half()[:, :64], w, y=y)
