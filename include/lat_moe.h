@@ -476,9 +476,8 @@ int lat_moe_ffn_fp8_ex(const void* x_fp8, const float* x_scales, const void* gat
  * At least one of y and y_q8_1 must be given; the type and stride of an array
  * that is NULL are not looked at.  Supported: T >= 0, T < 2^31, 1 <= N <=
  * LAT_MOE_DENSE_16_MAX_N, K % 8 == 0, 8 <= K <= 65536, ceil(T/64) *
- * ceil(N/64) < 2^31, strides < 2^31; pointers 16-byte aligned.  y and residual are read
- * and written 16 bytes at a time where N and their strides are multiples of 8.
- * A NaN or an infinity in x, w, bias or residual reaches the outputs that it
+ * ceil(N/64) < 2^31, strides < 2^31; pointers 16-byte aligned (the rows of y and residual
+ * may begin anywhere).  A NaN or an infinity in x, w, bias or residual reaches the outputs that it
  * enters and no others; a q8_1 block of 32 that holds a NaN output gets a NaN
  * as its scale d.  Beyond the case named, outputs must not overlap an input or
  * each other; what lies between the rows of y stays as it is.  T = 0 enqueues

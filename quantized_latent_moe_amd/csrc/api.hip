@@ -530,10 +530,9 @@ int lat_moe_dense_16(const void* x, int64_t x_stride, const void* w, int32_t typ
   int num_cus = 1;
   int rc = check_device(&num_cus);
   if (rc != LAT_MOE_OK) return rc;
-  const bool vec = N % 8 == 0 && (!y || y_stride % 8 == 0) && (!residual || residual_stride % 8 == 0);
   const Dense16Args a{x, w, T, x_stride, N, K, 0, 0,
                       {bias, residual, y, static_cast<uint8_t*>(y_q8_1), residual_stride, y_stride, residual_type,
-                       y_type, activation, N, vec}};
+                       y_type, activation, N}};
   if (launch_dense_16(a, type, false, num_cus, static_cast<hipStream_t>(stream)) != hipSuccess)
     return LAT_MOE_ELAUNCH;
   return LAT_MOE_OK;
@@ -551,8 +550,7 @@ int lat_moe_gated_16(const void* x, int64_t x_stride, const void* w, int32_t typ
   int rc = check_device(&num_cus);
   if (rc != LAT_MOE_OK) return rc;
   const Dense16Args a{x, w, T, x_stride, F, K, 0, 0,
-                      {bias, nullptr, h, nullptr, 0, h_stride, 0, h_type, activation, F,
-                       F % 8 == 0 && h_stride % 8 == 0}};
+                      {bias, nullptr, h, nullptr, 0, h_stride, 0, h_type, activation, F}};
   if (launch_dense_16(a, type, true, num_cus, static_cast<hipStream_t>(stream)) != hipSuccess) return LAT_MOE_ELAUNCH;
   return LAT_MOE_OK;
 }

@@ -33,23 +33,50 @@ constexpr Dense16Tile kDense16Tiles[] = {
 };
 constexpr int kDense16Variants = 8;
 
-// The variant with the least estimated time; steps: of K; weight_rows: gated
-// ones counted twice.
+// Estimated time of a launch; steps: of K; weight_rows: gated ones counted twice.
+inline float dense16_time(int variant, int64_t T, int64_t weight_rows, int steps, int num_cus) {
+  const Dense16Tile& v = kDense16Tiles[variant];
+  const int64_t tiles = v.count(T, weight_rows), slots = (int64_t)num_cus * v.per_cu;
+  const int64_t passes = tiles / slots, rest = tiles % slots;
+  float t = (float)passes * (v.full * (float)steps + v.tile);
+  if (rest) t += (rest <= num_cus ? v.alone : v.full) * (float)steps + v.tile;
+  return t;
+}
 inline int dense16_pick_tile(int64_t T, int64_t weight_rows, int steps, int num_cus) {
   int best = 0;
-  float least = 0.f;
+  for (int i = 1; i < kDense16Variants; ++i)
+    if (dense16_time(i, T, weight_rows, steps, num_cus) < dense16_time(best, T, weight_rows, steps, num_cus)) best = i;
+  return best;
+}
+
+// The first launch of a product: a tile, and for how many tokens.  Where large
+// tiles would leave most CUs idle in their last pass, they take the whole
+// passes, and the tokens that remain come in a launch of their own with the
+// tile that suits them (21000 x 4096 by 4096: five passes of 256 x 256 and 520
+// tokens in tiles of 128 x 128).
+struct Dense16Launch {
+  int variant;
+  int64_t tokens;
+};
+inline Dense16Launch dense16_plan(int64_t T, int64_t weight_rows, int steps, int num_cus) {
+  constexpr float kLaunch = 3.f;  // what a second launch costs
+  Dense16Launch plan{dense16_pick_tile(T, weight_rows, steps, num_cus), T};
+  float least = dense16_time(plan.variant, T, weight_rows, steps, num_cus);
   for (int i = 0; i < kDense16Variants; ++i) {
     const Dense16Tile& v = kDense16Tiles[i];
-    const int64_t tiles = v.count(T, weight_rows), slots = (int64_t)num_cus * v.per_cu;
-    const int64_t passes = tiles / slots, rest = tiles % slots;
-    float t = (float)passes * (v.full * (float)steps + v.tile);
-    if (rest) t += (rest <= num_cus ? v.alone : v.full) * (float)steps + v.tile;
-    if (i == 0 || t < least) {
-      best = i;
+    if (v.per_cu != 1) continue;
+    const int64_t columns = v.count(1, weight_rows), passes = v.count(T, weight_rows) / num_cus;
+    const int64_t tokens = passes * num_cus / columns * v.tokens;
+    if (tokens <= 0 || tokens >= T) continue;
+    const float t = (float)passes * (v.full * (float)steps + v.tile) + kLaunch +
+                    dense16_time(dense16_pick_tile(T - tokens, weight_rows, steps, num_cus), T - tokens, weight_rows,
+                                 steps, num_cus);
+    if (t < least) {
       least = t;
+      plan = Dense16Launch{i, tokens};
     }
   }
-  return best;
+  return plan;
 }
 
 // The kernel that streams the weights takes 4, 8 or 16 of them to a workgroup

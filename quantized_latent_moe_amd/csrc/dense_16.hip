@@ -275,8 +275,8 @@ hipError_t run(Dense16Args a, hipStream_t st) {
 }
 
 template <int TYPE, bool GATED>
-hipError_t launch(const Dense16Args& a, int num_cus, hipStream_t st) {
-  switch (dense16_pick_tile(a.T, (GATED ? 2 : 1) * (int64_t)a.N, (a.K + kStep - 1) / kStep, num_cus)) {
+hipError_t run_variant(int variant, const Dense16Args& a, hipStream_t st) {
+  switch (variant) {
     case 0: return run<0, TYPE, 8, 4, 2, 4, 1, GATED, 2>(a, st);
     case 1: return run<1, TYPE, 8, 3, 2, 4, 1, GATED, 2>(a, st);
     case 2: return run<2, TYPE, 8, 2, 2, 4, 1, GATED, 3>(a, st);
@@ -288,10 +288,34 @@ hipError_t launch(const Dense16Args& a, int num_cus, hipStream_t st) {
   }
 }
 
+// `p` of `type` at a row.
+const char* row_of(const void* p, int type, int64_t row, int64_t stride) {
+  return static_cast<const char*>(p) + row * stride * (type == LAT_MOE_F32 ? 4 : 2);
+}
+
+template <int TYPE, bool GATED>
+hipError_t launch(Dense16Args a, int num_cus, hipStream_t st) {
+  const int64_t weight_rows = (GATED ? 2 : 1) * (int64_t)a.N, T = a.T;
+  if (dense16_small(T, weight_rows, num_cus)) return launch_dense_16_small(a, TYPE, GATED, num_cus, st);
+  const int steps = (a.K + kStep - 1) / kStep;
+  int64_t left = T;
+  while (left) {
+    const Dense16Launch plan = dense16_plan(left, weight_rows, steps, num_cus);
+    a.T = plan.tokens;
+    const hipError_t rc = run_variant<TYPE, GATED>(plan.variant, a, st);
+    if (rc != hipSuccess) return rc;
+    left -= plan.tokens;
+    a.x = row_of(a.x, TYPE, plan.tokens, a.x_stride);
+    if (a.e.residual) a.e.residual = row_of(a.e.residual, a.e.residual_type, plan.tokens, a.e.residual_stride);
+    if (a.e.y) a.e.y = const_cast<char*>(row_of(a.e.y, a.e.y_type, plan.tokens, a.e.y_stride));
+    if (a.e.y_q8) a.e.y_q8 += plan.tokens * (a.N / 32) * kQ81Bytes;
+  }
+  return hipSuccess;
+}
+
 }  // namespace
 
 hipError_t launch_dense_16(const Dense16Args& a, int type, bool gated, int num_cus, hipStream_t st) {
-  if (dense16_small(a.T, (gated ? 2 : 1) * (int64_t)a.N, num_cus)) return launch_dense_16_small(a, type, gated, num_cus, st);
   if (type == LAT_MOE_BF16)
     return gated ? launch<LAT_MOE_BF16, true>(a, num_cus, st) : launch<LAT_MOE_BF16, false>(a, num_cus, st);
   return gated ? launch<LAT_MOE_F16, true>(a, num_cus, st) : launch<LAT_MOE_F16, false>(a, num_cus, st);

@@ -63,7 +63,10 @@ __device__ __forceinline__ void store1(void* base, int type, int64_t elem, float
   if (type == LAT_MOE_F32) static_cast<float*>(base)[elem] = v;
   else static_cast<uint16_t*>(base)[elem] = (uint16_t)(type == LAT_MOE_BF16 ? pack_bf16(v, v) : pack_f16(v, v));
 }
-typedef float v4f_unaligned __attribute__((ext_vector_type(4), aligned(4)));
+// Pieces of rows that begin anywhere (rows of an odd length): the memory takes
+// 16 bytes at any address of the element's alignment.
+typedef float v4f_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t v4u_any __attribute__((ext_vector_type(4), aligned(2)));
 
 // The 8 columns from n on of a row of `count` columns (those past it: zeros).
 __device__ __forceinline__ void load_bias8(const float* bias, int n, int count, float* b) {
@@ -73,7 +76,7 @@ __device__ __forceinline__ void load_bias8(const float* bias, int n, int count, 
   if (live >= 8) {
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
-      const v4f_unaligned p = *reinterpret_cast<const v4f_unaligned*>(bias + n + i);
+      const v4f_any p = *reinterpret_cast<const v4f_any*>(bias + n + i);
       b[i] = p[0];
       b[i + 1] = p[1];
       b[i + 2] = p[2];
@@ -86,40 +89,53 @@ __device__ __forceinline__ void load_bias8(const float* bias, int n, int count, 
 }
 
 // Eight values of a type known at run time, as they lie in memory.
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 struct Piece8 {
-  uint4 a, b;  // b: fp32 only
+  v4u a, b;  // b: fp32 only
   __device__ __forceinline__ void load(const void* base, int type, int64_t elem) {
     if (type == LAT_MOE_F32) {
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + elem);
+      const v4u_any* p = reinterpret_cast<const v4u_any*>(static_cast<const float*>(base) + elem);
       a = p[0];
       b = p[1];
     } else {
-      a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + elem);
+      a = *reinterpret_cast<const v4u_any*>(static_cast<const uint16_t*>(base) + elem);
     }
   }
   __device__ __forceinline__ void add_to(int type, float* v) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w}, u[4] = {b.x, b.y, b.z, b.w};
     if (type == LAT_MOE_F32) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[i] += __builtin_bit_cast(float, w[i]);
-        v[4 + i] += __builtin_bit_cast(float, u[i]);
+        v[i] += __builtin_bit_cast(float, (uint32_t)a[i]);
+        v[4 + i] += __builtin_bit_cast(float, (uint32_t)b[i]);
       }
     } else if (type == LAT_MOE_BF16) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[2 * i] += __builtin_bit_cast(float, w[i] << 16);
-        v[2 * i + 1] += __builtin_bit_cast(float, w[i] & 0xffff0000u);
+        v[2 * i] += __builtin_bit_cast(float, (uint32_t)a[i] << 16);
+        v[2 * i + 1] += __builtin_bit_cast(float, (uint32_t)a[i] & 0xffff0000u);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[2 * i] += half_bits_to_float(w[i] & 0xffffu);
-        v[2 * i + 1] += half_bits_to_float(w[i] >> 16);
+        v[2 * i] += half_bits_to_float(a[i] & 0xffffu);
+        v[2 * i + 1] += half_bits_to_float(a[i] >> 16);
       }
     }
   }
 };
+__device__ __forceinline__ void store8_any(void* base, int type, int64_t elem, const float* v) {
+  if (type == LAT_MOE_F32) {
+    v4f_any* p = reinterpret_cast<v4f_any*>(static_cast<float*>(base) + elem);
+    p[0] = v4f_any{v[0], v[1], v[2], v[3]};
+    p[1] = v4f_any{v[4], v[5], v[6], v[7]};
+  } else {
+    const bool bf = type == LAT_MOE_BF16;
+    v4u_any w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = bf ? pack_bf16(v[2 * i], v[2 * i + 1]) : pack_f16(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<v4u_any*>(static_cast<uint16_t*>(base) + elem) = w;
+  }
+}
 
 // q8_1 block of a row of 32 columns that four neighbouring lanes hold, 8 each.
 __device__ __forceinline__ void store_q8(uint8_t* block, const float* v, int part, bool live) {
@@ -174,11 +190,11 @@ struct TileEpilogue {
     float b[8], bu[8];
     load_bias8(e.bias, n, e.N, b);
     if (GATED) load_bias8(e.bias ? e.bias + e.N : nullptr, n, e.N, bu);
-    const bool inside = n < e.N, pieces = e.vec && e.residual && inside;
+    const bool inside = n < e.N, whole = n + 8 <= e.N;
     Piece8 ahead[kPasses];
     auto fetch = [&](int j, int p) {
       const int tl = 16 * j + kRows * p + row;
-      if (pieces && tl < live) ahead[p].load(e.residual, e.residual_type, (t0 + tl) * e.residual_stride + n);
+      if (e.residual && whole && tl < live) ahead[p].load(e.residual, e.residual_type, (t0 + tl) * e.residual_stride + n);
     };
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) fetch(0, p);
@@ -218,11 +234,11 @@ struct TileEpilogue {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = reinterpret_cast<v4f*>(at)[i / 4][i % 4];
         if (stored) {
-          if (e.vec) {
+          if (whole) {
             if (e.residual) ahead[p].add_to(e.residual_type, v);
-            if (e.y) store8(e.y, e.y_type, t * e.y_stride + n, v);
+            if (e.y) store8_any(e.y, e.y_type, t * e.y_stride + n, v);
           } else {
-            const int count = min(8, e.N - n);
+            const int count = e.N - n;
 #pragma unroll 1
             for (int i = 0; i < count; ++i) {
               float u = at[i];

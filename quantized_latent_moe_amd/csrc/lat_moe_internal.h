@@ -303,7 +303,6 @@ struct Epilogue16 {
   int64_t residual_stride, y_stride;
   int residual_type, y_type, act;
   int N;                 // columns of y
-  bool vec;              // rows of y and of the residual are whole pieces of 8 values
 };
 struct Dense16Args {
   const void* x;
