@@ -59,7 +59,10 @@ struct Dense16Launch {
   int64_t tokens;
 };
 inline Dense16Launch dense16_plan(int64_t T, int64_t weight_rows, int steps, int num_cus) {
-  constexpr float kLaunch = 3.f;  // what a second launch costs
+  // What a second launch costs, so that it is made where it gains for certain
+  // (us with it | without): 21000 x 4096 by 4096 566 | 605, 5268 x 4096 by 16384
+  // 543 | 569, but 5268 x 4096 by 4096 149 | 143.
+  constexpr float kLaunch = 8.f;
   Dense16Launch plan{dense16_pick_tile(T, weight_rows, steps, num_cus), T};
   float least = dense16_time(plan.variant, T, weight_rows, steps, num_cus);
   for (int i = 0; i < kDense16Variants; ++i) {
