@@ -257,7 +257,7 @@ __global__ __launch_bounds__(64 * WN * WT * WK) void k_dense_16(const Dense16Arg
     __syncthreads();  // the epilogue takes other parts
     if (wk > 0) return;
   }
-  E::run(a.e, acc, reinterpret_cast<float*>(stages + wave * E::kBytes), at.n0 + wn * E::OUT, at.t0 + wt * 16 * FB,
+  E::template run<TYPE>(a.e, acc, reinterpret_cast<float*>(stages + wave * E::kBytes), at.n0 + wn * E::OUT, at.t0 + wt * 16 * FB,
          at.t_live - wt * 16 * FB, lane);
 }
 

@@ -185,15 +185,124 @@ struct TileEpilogue {
   static constexpr int kBytes = 16 * kPitch * 4;        // of LDS for a wave
   static_assert(64 % kLanes == 0 && 16 % kRows == 0, "whole rows");
 
-  // n0: the wave's first column; t0: its first token; live: its tokens inside the matrix.
-  static __device__ __forceinline__ void run(const Epilogue16& e, const v4f (&acc)[FA][FB], float* lds, int n0,
-                                             int64_t t0, int live, int lane) {
-    const int r = lane & 15, g = lane >> 4;
-    const int c = (lane % kLanes) * 8, row = lane / kLanes, n = n0 + c;
-    const bool shape = GATED || e.bias || e.act != LAT_MOE_ACT_NONE;
+  // Bias, activation and the gated product of the 16 tokens in LDS, in place.
+  static __device__ __forceinline__ void shape(const Epilogue16& e, float* lds, int n, int lane) {
+    const int c = (lane % kLanes) * 8, row = lane / kLanes;
     float b[8], bu[8];
     load_bias8(e.bias, n, e.N, b);
     if (GATED) load_bias8(e.bias ? e.bias + e.N : nullptr, n, e.N, bu);
+#pragma unroll 1
+    for (int p = 0; p < kPasses; ++p) {
+      v4f* at = reinterpret_cast<v4f*>(lds + (kRows * p + row) * kPitch + c);
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = at[i / 4][i % 4] + b[i];
+      activate<8>(v, e.act);
+      if constexpr (GATED) {
+        const v4f* up = reinterpret_cast<const v4f*>(lds + (kRows * p + row) * kPitch + OUT + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= up[i / 4][i % 4] + bu[i];
+      }
+      at[0] = v4f{v[0], v[1], v[2], v[3]};
+      at[1] = v4f{v[4], v[5], v[6], v[7]};
+    }
+  }
+  static __device__ __forceinline__ bool shapes(const Epilogue16& e) {
+    return GATED || e.bias || e.act != LAT_MOE_ACT_NONE;
+  }
+
+  // A wave's part that lies inside the matrix whole, with y of type YT (none:
+  // q8_1 alone) and a residual of type RT (or none): types and places are known
+  // here, and pointers go from row to row.  The general form below takes 50 VALU
+  // operations for each 8 columns, 4 us for a tile of 256 x 256; this one 15.
+  static constexpr int kNone = -1;
+  template <int YT, int RT>
+  static __device__ __forceinline__ void run_whole(const Epilogue16& e, const v4f (&acc)[FA][FB], float* lds, int n0,
+                                                   int64_t t0, int lane) {
+    const int r = lane & 15, g = lane >> 4;
+    const int c = (lane % kLanes) * 8, row = lane / kLanes, n = n0 + c;
+    constexpr int kDepth = RT == LAT_MOE_F32 ? 1 : 3;  // 16 tokens' residual on their way
+    constexpr int kSizeY = YT == LAT_MOE_F32 ? 4 : 2, kSizeR = RT == LAT_MOE_F32 ? 4 : 2;
+    Piece8 ahead[kDepth][kPasses];
+    const int64_t step_y = kRows * e.y_stride * kSizeY, step_r = kRows * e.residual_stride * kSizeR;
+    char* y = YT == kNone ? nullptr : static_cast<char*>(e.y) + ((t0 + row) * e.y_stride + n) * kSizeY;
+    const char* res = nullptr;
+    if (RT != kNone) res = static_cast<const char*>(e.residual) + ((t0 + row) * e.residual_stride + n) * kSizeR;
+    auto fetch = [&](int j) {
+      if constexpr (RT != kNone) {
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+          ahead[j % kDepth][p].load(res, RT, 0);
+          res += step_r;
+        }
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < kDepth && j < FB; ++j) fetch(j);
+#pragma unroll 1
+    for (int j = 0; j < FB; ++j) {
+      int turn = j;  // not to be taken for an index, which registers do not have
+      asm("" : "+s"(turn));
+      Piece8 now[kPasses];
+#pragma unroll
+      for (int q = 0; q < FB; ++q)
+        if (q == turn) {
+#pragma unroll
+          for (int i = 0; i < FA; ++i) *reinterpret_cast<v4f*>(lds + r * kPitch + 16 * i + 4 * g) = acc[i][q];
+          if constexpr (RT != kNone) {
+#pragma unroll
+            for (int p = 0; p < kPasses; ++p) now[p] = ahead[q % kDepth][p];
+          }
+          if (q + kDepth < FB) fetch(q + kDepth);
+        }
+      if (shapes(e)) shape(e, lds, n, lane);
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const v4f* at = reinterpret_cast<const v4f*>(lds + (kRows * p + row) * kPitch + c);
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = at[i / 4][i % 4];
+        if constexpr (RT != kNone) now[p].add_to(RT, v);
+        if constexpr (YT != kNone) {
+          store8_any(y, YT, 0, v);
+          y += step_y;
+        } else if constexpr (!GATED) {
+          const int64_t t = t0 + 16 * j + kRows * p + row;
+          store_q8(e.y_q8 + (t * (e.N / 32) + n / 32) * kQ81Bytes, v, lane & 3, true);
+        }
+      }
+    }
+  }
+
+  // n0: the wave's first column; t0: its first token; live: its tokens inside
+  // the matrix; TYPE: the operands' type.
+  template <int TYPE>
+  static __device__ __forceinline__ void run(const Epilogue16& e, const v4f (&acc)[FA][FB], float* lds, int n0,
+                                             int64_t t0, int live, int lane) {
+    if (live >= 16 * FB && n0 + OUT <= e.N) {
+      if (GATED || !e.y_q8) {
+        if (GATED || !e.residual) {
+          if (e.y_type == TYPE) return run_whole<TYPE, kNone>(e, acc, lds, n0, t0, lane);
+          if (e.y_type == LAT_MOE_F32) return run_whole<LAT_MOE_F32, kNone>(e, acc, lds, n0, t0, lane);
+        } else if constexpr (!GATED) {
+          if (e.y_type == TYPE && e.residual_type == TYPE) return run_whole<TYPE, TYPE>(e, acc, lds, n0, t0, lane);
+          if (e.y_type == TYPE && e.residual_type == LAT_MOE_F32)
+            return run_whole<TYPE, LAT_MOE_F32>(e, acc, lds, n0, t0, lane);
+          if (e.y_type == LAT_MOE_F32 && e.residual_type == LAT_MOE_F32)
+            return run_whole<LAT_MOE_F32, LAT_MOE_F32>(e, acc, lds, n0, t0, lane);
+        }
+      } else if constexpr (!GATED) {
+        if (!e.y && !e.residual) return run_whole<kNone, kNone>(e, acc, lds, n0, t0, lane);
+      }
+    }
+    run_any(e, acc, lds, n0, t0, live, lane);
+  }
+
+  // Any other part: at the matrix's ends, q8_1 beside y, mixed types.
+  static __device__ __forceinline__ void run_any(const Epilogue16& e, const v4f (&acc)[FA][FB], float* lds, int n0,
+                                                 int64_t t0, int live, int lane) {
+    const int r = lane & 15, g = lane >> 4;
+    const int c = (lane % kLanes) * 8, row = lane / kLanes, n = n0 + c;
     const bool inside = n < e.N, whole = n + 8 <= e.N;
     Piece8 ahead[kPasses];
     auto fetch = [&](int j, int p) {
@@ -205,29 +314,15 @@ struct TileEpilogue {
 #pragma unroll 1
     for (int j = 0; j < FB; ++j) {
       if (16 * j >= live) break;  // the whole wave
+      int turn = j;
+      asm("" : "+s"(turn));
 #pragma unroll
       for (int q = 0; q < FB; ++q)
-        if (q == j) {
+        if (q == turn) {
 #pragma unroll
           for (int i = 0; i < FA; ++i) *reinterpret_cast<v4f*>(lds + r * kPitch + 16 * i + 4 * g) = acc[i][q];
         }
-      if (shape) {
-#pragma unroll 1
-        for (int p = 0; p < kPasses; ++p) {
-          v4f* at = reinterpret_cast<v4f*>(lds + (kRows * p + row) * kPitch + c);
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = at[i / 4][i % 4] + b[i];
-          activate<8>(v, e.act);
-          if constexpr (GATED) {
-            const v4f* up = reinterpret_cast<const v4f*>(lds + (kRows * p + row) * kPitch + OUT + c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= up[i / 4][i % 4] + bu[i];
-          }
-          at[0] = v4f{v[0], v[1], v[2], v[3]};
-          at[1] = v4f{v[4], v[5], v[6], v[7]};
-        }
-      }
+      if (shapes(e)) shape(e, lds, n, lane);
 #pragma unroll
       for (int p = 0; p < kPasses; ++p) {
         const int tl = 16 * j + kRows * p + row;
