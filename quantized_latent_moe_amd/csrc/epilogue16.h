@@ -241,14 +241,14 @@ struct TileEpilogue {
     for (int j = 0; j < kDepth && j < FB; ++j) fetch(j);
 #pragma unroll 1
     for (int j = 0; j < FB; ++j) {
-      int turn = j;  // not to be taken for an index, which registers do not have
-      asm("" : "+s"(turn));
       Piece8 now[kPasses];
 #pragma unroll
       for (int q = 0; q < FB; ++q)
-        if (q == turn) {
+        if (q == j) {
 #pragma unroll
           for (int i = 0; i < FA; ++i) *reinterpret_cast<v4f*>(lds + r * kPitch + 16 * i + 4 * g) = acc[i][q];
+          // keeps the branches apart: merged, they would need registers with an index
+          asm volatile("; turn %0" ::"n"(q));
           if constexpr (RT != kNone) {
 #pragma unroll
             for (int p = 0; p < kPasses; ++p) now[p] = ahead[q % kDepth][p];
@@ -314,13 +314,13 @@ struct TileEpilogue {
 #pragma unroll 1
     for (int j = 0; j < FB; ++j) {
       if (16 * j >= live) break;  // the whole wave
-      int turn = j;
-      asm("" : "+s"(turn));
 #pragma unroll
       for (int q = 0; q < FB; ++q)
-        if (q == turn) {
+        if (q == j) {
 #pragma unroll
           for (int i = 0; i < FA; ++i) *reinterpret_cast<v4f*>(lds + r * kPitch + 16 * i + 4 * g) = acc[i][q];
+          // keeps the branches apart: merged, they would need registers with an index
+          asm volatile("; turn %0" ::"n"(q));
         }
       if (shapes(e)) shape(e, lds, n, lane);
 #pragma unroll
