@@ -21,17 +21,17 @@ struct Dense16Tile {
 };
 
 constexpr Dense16Tile kDense16Tiles[] = {
-    // 21000 x 4096 by 4096 | 5268 x 4096 by 1024 | 517 x 2056 by 4104 | 512 x 4096 by 4096 (us):
-    {256, 256, 1, 1.45f, 1.13f, 5.f},  // 597 | 77 | 55 | 73
-    {256, 192, 1, 1.27f, 0.92f, 5.f},  // 611 | 64 | 47 | 62
-    {256, 128, 1, 0.87f, 0.66f, 4.f},  // 630 | 53 | 35 | 45
-    {128, 128, 1, 0.51f, 0.42f, 3.f},  // 783 | 60 | 24 | 30
-    {128, 128, 2, 0.96f, 0.60f, 4.f},  // 697 | 53 | 28 | 39: the same with fewer stages, two on a CU
-    {128, 64, 2, 0.66f, 0.28f, 4.f},   // 920 | 60 | 31 | 22
-    {64, 64, 2, 0.37f, 0.21f, 3.f},    // 1024 | 71 | 29 | 29
-    {64, 32, 1, 0.145f, 0.12f, 3.f},   // K dealt to four slices of waves; 512 x 4096 by 1024 12.6 (64 x 64: 15)
+    // 21000 x 4096 by 4096 | 5268 x 4096 by 1024 | 517 x 2056 by 4100 | 512 x 4096 by 4096, bf16 (us):
+    {256, 256, 1, 1.47f, 1.07f, 4.f},  // 593 | 74 | 52 | 71
+    {256, 192, 1, 1.24f, 0.88f, 4.f},  // 602 | 61 | 45 | 59
+    {256, 128, 1, 0.84f, 0.64f, 4.f},  // 637 | 49 | 33 | 43
+    {128, 128, 1, 0.52f, 0.39f, 3.f},  // 777 | 60 | 24 | 28
+    {128, 64, 2, 0.62f, 0.29f, 4.f},   // 920 | 56 | 30 | 23
+    {64, 64, 2, 0.33f, 0.19f, 3.f},    // 1024 | 70 | 29 | 27
+    // K dealt to four slices of waves: 512 x 4096 by 1024 takes 11.6 us (64 x 64: 15)
+    {64, 32, 1, 0.145f, 0.12f, 3.f},   // 1641 | 114 | 40 | 43
 };
-constexpr int kDense16Variants = 8;
+constexpr int kDense16Variants = 7;
 
 // Estimated time of a launch; steps: of K; weight_rows: gated ones counted twice.
 inline float dense16_time(int variant, int64_t T, int64_t weight_rows, int steps, int num_cus) {

@@ -281,10 +281,9 @@ hipError_t run_variant(int variant, const Dense16Args& a, hipStream_t st) {
     case 1: return run<1, TYPE, 8, 3, 2, 4, 1, GATED, 2>(a, st);
     case 2: return run<2, TYPE, 8, 2, 2, 4, 1, GATED, 3>(a, st);
     case 3: return run<3, TYPE, 4, 2, 2, 4, 1, GATED, 4>(a, st);
-    case 4: return run<4, TYPE, 4, 2, 2, 4, 1, GATED, 2>(a, st);
-    case 5: return run<5, TYPE, 4, 1, 2, 4, 1, GATED, 3>(a, st);
-    case 6: return run<6, TYPE, 4, 1, 1, 4, 1, GATED, 4>(a, st);
-    default: return run<7, TYPE, 4, 1, 1, 2, 4, GATED, 3>(a, st);
+    case 4: return run<4, TYPE, 4, 1, 2, 4, 1, GATED, 3>(a, st);
+    case 5: return run<5, TYPE, 4, 1, 1, 4, 1, GATED, 4>(a, st);
+    default: return run<6, TYPE, 4, 1, 1, 2, 4, GATED, 3>(a, st);
   }
 }
 
@@ -295,11 +294,12 @@ const char* row_of(const void* p, int type, int64_t row, int64_t stride) {
 
 template <int TYPE, bool GATED>
 hipError_t launch(Dense16Args a, int num_cus, hipStream_t st) {
-  const int64_t weight_rows = (GATED ? 2 : 1) * (int64_t)a.N, T = a.T;
-  if (dense16_small(T, weight_rows, num_cus)) return launch_dense_16_small(a, TYPE, GATED, num_cus, st);
+  const int64_t weight_rows = (GATED ? 2 : 1) * (int64_t)a.N;
   const int steps = (a.K + kStep - 1) / kStep;
-  int64_t left = T;
+  int64_t left = a.T;
   while (left) {
+    a.T = left;
+    if (dense16_small(left, weight_rows, num_cus)) return launch_dense_16_small(a, TYPE, GATED, num_cus, st);
     const Dense16Launch plan = dense16_plan(left, weight_rows, steps, num_cus);
     a.T = plan.tokens;
     const hipError_t rc = run_variant<TYPE, GATED>(plan.variant, a, st);

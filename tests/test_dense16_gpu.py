@@ -23,6 +23,7 @@ if not torch.cuda.is_available():
 
 import quantized_latent_moe_amd as lm  # noqa: E402
 from oracle import rows16  # noqa: E402
+from tests import _tiles16  # noqa: E402
 
 TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 U = 2.0 ** -23
@@ -104,6 +105,60 @@ def test_gated_whole_numbers(T, N, K, kind):
         torch.cuda.synchronize()
         assert torch.equal(h, ref.float().to(TYPES[out])), (out, extra)
         _untouched(h, big)
+
+
+@pytest.mark.parametrize("case,variants", _tiles16.RAGGED, ids=str)
+def test_every_tile_whole_numbers(case, variants):
+    """Each tile, and two launches in a row, with ragged ends: both products, bit for bit."""
+    T, N, K = case
+    g = _gen(T + N + K)
+    kind, other = (torch.bfloat16, torch.float16) if T % 2 else (torch.float16, torch.bfloat16)
+    x, w = _ints(g, (T, K), -3, 3).to(kind), _ints(g, (N, K), -1, 1)
+    w *= torch.rand(w.shape, generator=g, device="cuda") < min(1.0, 600 / K)
+    w, bias, res = w.to(kind), _ints(g, (N,), -50, 50), _ints(g, (T, N), -90, 90)
+    v, mag = rows16.product(x, w, bias)
+    assert mag.max() < 4096
+    xa, _ = _apart(x, 8)
+    # plain, then with everything and rows of an odd length: fp32 from fp32, the operands' type from it, the other one
+    y, big = _out(T, N, "f32", 1)
+    lm.dense_16(xa, w, bias=bias, y=y)
+    torch.cuda.synchronize()
+    assert torch.equal(y.double(), v)
+    _untouched(y, big)
+    del y, big
+    ref = (rows16.activation(v, "relu") + res).float()
+    for out in (torch.float32, kind, other):
+        y, big = _apart(res.to(out), 3)
+        lm.dense_16(x, w, bias=bias, activation="relu", residual=y, y=y)
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref.to(out)), out
+        _untouched(y, big)
+    y = torch.empty(T, N, dtype=kind, device="cuda")
+    lm.dense_16(x, w, bias=bias, activation="relu", residual=res, y=y)
+    torch.cuda.synchronize()
+    assert torch.equal(y, ref.to(kind))
+    F = N // 2
+    ref = (rows16.activation(v[:, :F], "relu") * v[:, F:]).float()
+    for out in (torch.float32, kind):
+        h, big = _apart(torch.full((T, F), float("nan"), dtype=out, device="cuda"), 5)
+        lm.gated_16(xa, w, h, bias=bias, activation="relu")
+        torch.cuda.synchronize()
+        assert torch.equal(h, ref.to(out)), out
+        _untouched(h, big)
+
+
+@pytest.mark.parametrize("T,N,K", [(6007, 1312, 72), (3135, 1312, 72), (329, 5760, 72), (914, 4256, 80), (497, 3968, 712),
+                                   (508, 992, 688), (4133, 4128, 2056)], ids=str)
+def test_q8_1_rows_of_every_tile(T, N, K):
+    g = _gen(T)
+    x, w = torch.randn(T, K, generator=g, device="cuda").half(), torch.randn(N, K, generator=g, device="cuda").half()
+    y, q = torch.empty(T, N, device="cuda"), torch.full((T, N // 32, 36), 9, dtype=torch.uint8, device="cuda")
+    beside, want = q.clone(), q.clone()
+    lm.dense_16(x, w, y_q8_1=q)
+    lm.dense_16(x, w, y=y, y_q8_1=beside)
+    lm.quantize_q8_1(y, want)
+    torch.cuda.synchronize()
+    assert torch.equal(q, want) and torch.equal(beside, want)
 
 
 def _act_tol(v, e):
