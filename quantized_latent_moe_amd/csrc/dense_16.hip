@@ -4,8 +4,42 @@
 //
 //   y[t][n] = act(sum over k of x[t][k] w[n][k] + bias[n]) + residual[t][n]
 //   h[t][f] = act(gate) * up
-#include <algorithm>
-
+//
+// One workgroup computes TN = 16 FA WN weight rows x TT = 16 FB WT tokens;
+// gated tiles hold gate rows and the same columns' up rows, so that one lane
+// has both.  Weights are the MFMA's row operand: a lane then holds four
+// neighbouring weight rows of one token.  Products are exact and added in fp32
+// by the MFMA.
+//
+// Per K step of 64 both tiles go to LDS by direct loads (16 bytes a lane, no
+// registers), STAGES steps ahead; a row is 128 bytes, its 16-byte chunks
+// XOR-swizzled by the row so that fragment reads have no bank conflicts (none
+// counted; the swizzle is applied to the global address of a lane, since the
+// LDS side of a direct load is linear).  Fragments are read a step ahead into
+// the registers that their last MFMA has left, and the step's one barrier comes
+// after its first MFMAs, when the reads are long done: nothing waits for LDS.
+// The loads come at every third MFMA of a step's first half: they have to land
+// within a step (8192^3 takes 767 us; with a load at every fourth MFMA 788, at
+// every sixth 810, and at every second 2% more too: the memory pipe then makes
+// the waves wait).
+// Steps of 32 with twice the stages take 10% longer (a barrier for half the
+// work), two workgroups of half the tile on a CU 25% (more bytes for a product),
+// and four waves of 128 x 128 in twice the registers as long.
+//
+// Where few tiles would have all of K to go, WK slices of waves deal the steps
+// among themselves, each with stages of its own, and add their sums in LDS at
+// the end, in their order: a step of one slice is a chain of barrier, reads and
+// MFMAs of 0.19 us, whatever it multiplies.
+//
+// What bounds it: large products the power that the chip may draw.  Under
+// 21000 x 4096 by 4096 the clock falls to 1.8 GHz with the matrix pipes busy 65
+// to 73% of the cycles; the loop alone, without the loads, runs at 1700 TF.
+// 21000 x 4096 by 4096 with residual takes 565 to 590 us (1190 to 1250 TF; a
+// library product without it 570 to 615 on the same machines), the gated pair
+// 5268 x 4096 by 2 x 8192 525 to 545 us (1300 to 1350 TF), 8192^3 765 us
+// (1430 TF; the library 675 to 750).  Mid-sized ones are bound by what a CU
+// loads, 75 to 100 GB/s with all of them at it: 5268 x 4096 by 1024 takes 50 us
+// (870 TF), 517 x 2056 by 4100 25 us, 5268 x 4096 by 128 15 us.
 #include "dense16_tiles.h"
 #include "epilogue16.h"
 
