@@ -449,7 +449,8 @@ int lat_moe_ffn_fp8_ex(const void* x_fp8, const float* x_scales, const void* gat
 
 /* Activations, in fp32:
  *   NONE v;  RELU max(v, 0), a NaN stays one;  SILU v / (1 + exp(-v));
- *   GELU v (1 + erf(v / sqrt 2)) / 2, within 1e-7 |v|;
+ *   GELU v (1 + erf(v / sqrt 2)) / 2, within 1e-7 |v|, for v >= -6 also within
+ *     1e-5 of itself;
  *   GELU_TANH v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
 #define LAT_MOE_ACT_NONE 0
 #define LAT_MOE_ACT_RELU 1
