@@ -16,6 +16,7 @@
 // tokens the rounds, one behind the other (4 x 128 5.1 us, without groups 4.1).
 // A wave for each token takes 36 to 44 us for 21000 x 256, and 5.8 for 4 x 128.
 #include "block_fp8.h"
+#include "exp64.h"
 
 namespace latmoe {
 namespace {
@@ -60,27 +61,21 @@ __device__ __forceinline__ float unordered(int k) {
   return __builtin_bit_cast(float, k ^ ((k >> 31) & 0x7fffffff));
 }
 
-// exp(x), |x| <= 700, within 2^-51: x = n ln 2 + r, and the polynomial of degree
-// 10 through exp at the Chebyshev points of |r| <= ln 2 / 2.  The coefficients
-// are kept in scalar registers, which a multiply-add can read; as constants the
-// compiler moves each of them, twice 32 bits, before each use.
+// exp(x), |x| <= 700.  The coefficients are kept in scalar registers, which a
+// multiply-add can read; as constants the compiler moves each of them, twice 32
+// bits, before each use.
 struct Exp64 {
-  double c[10];
-  __device__ __forceinline__ Exp64()
-      : c{2.7626357241447223e-07, 2.764018079620985e-06, 2.4801504346997686e-05, 0.00019841170270440067,
-          0.0013888888932488599,  0.008333333385667782,  0.04166666666657314,    0.16666666666554406,
-          0.5000000000000006,     1.0000000000000067} {
+  double c[kExp64Coefficients];
+  __device__ __forceinline__ Exp64() {
 #pragma unroll
-    for (int i = 0; i < 10; ++i) asm("" : "+s"(c[i]));
+    for (int i = 0; i < kExp64Coefficients; ++i) {
+      c[i] = kExp64[i];
+      asm("" : "+s"(c[i]));
+    }
   }
   __device__ __forceinline__ double operator()(double x) const {
-    const double n = __builtin_rint(x * 0x1.71547652b82fep+0);
-    const double r = __builtin_fma(n, -0x1.62e42fefa39efp-1, x);
-    double p = __builtin_fma(c[0], r, c[1]);
-#pragma unroll
-    for (int i = 2; i < 10; ++i) p = __builtin_fma(p, r, c[i]);
-    p = __builtin_fma(p, r, 1.0);
-    return __builtin_amdgcn_ldexp(p, (int)n);
+    const double n = exp64_power(x);
+    return __builtin_amdgcn_ldexp(exp64_series(c, exp64_rest(x, n)), (int)n);
   }
 };
 // 1 / d, 0 < d <= e^700: the hardware's estimate (at least 20 bits) and two steps that double them.
