@@ -38,7 +38,8 @@ __device__ __forceinline__ float gelu(float v) {
   p = fmaf(p, x, 0x1.addc56p-5f);
   p = fmaf(p, x, 0x1.d63b9cp-2f);
   p = fmaf(p, x, 0x1.26aed2p+0f);
-  const float e = __builtin_amdgcn_exp2f(-(x * p)), half = 0.5f * v;
+  // the largest finite half: infinity times a tail of 0 would be a NaN
+  const float e = __builtin_amdgcn_exp2f(-(x * p)), half = fminf(0.5f * v, 0x1.fffffep+127f);
   return v < 0.f ? half * e : fmaf(-half, e, v);
 }
 

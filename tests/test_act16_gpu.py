@@ -86,3 +86,28 @@ def test_gelu_of_every_size():
         ref, tol = _reference(part, "gelu")
         bad = (y[0].double() - ref).abs() > tol
         assert not bad.any(), (int(bad.sum()), part[bad][:4].tolist(), ((y[0].double() - ref).abs() / part.abs()).max().item())
+
+
+@pytest.mark.parametrize("case,variants", [((300, 514, 72), [6]), ((329, 5746, 72), [3]), ((4, 514, 72), [-1])], ids=str)
+def test_infinite_sums(case, variants):
+    """v of +inf stays, of -inf is what the formula gives (-inf times 0), NaN stays; their neighbours are as without them."""
+    T, N, K = case
+    assert [v for v, _ in _tiles16.launches(T, N, K)] == variants
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x, w = torch.randn(T, K, generator=g, device="cuda").half(), torch.randn(N, K, generator=g, device="cuda").half()
+    bias = torch.zeros(N, device="cuda")
+    there = [(3, math.inf), (200, -math.inf), (N - 1, math.nan), (N - 2, math.inf)]
+    for act in ("none", "relu", "silu", "gelu", "gelu_tanh"):
+        y, want = torch.empty(T, N, device="cuda"), torch.empty(T, N, device="cuda")
+        lm.dense_16(x, w, bias=bias, activation=act, y=want)
+        at = bias.clone()
+        for n, value in there:
+            at[n] = value
+        lm.dense_16(x, w, bias=at, activation=act, y=y)
+        torch.cuda.synchronize()
+        assert (y[:, [3, N - 2]] == math.inf).all() and torch.isnan(y[:, N - 1]).all(), act
+        low = y[:, 200]
+        assert {"none": low == -math.inf, "relu": low == 0}.get(act, torch.isnan(low)).all(), act
+        rest = torch.ones(N, dtype=torch.bool, device="cuda")
+        rest[[n for n, _ in there]] = False
+        assert torch.equal(y[:, rest], want[:, rest])
