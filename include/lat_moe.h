@@ -451,7 +451,11 @@ int lat_moe_ffn_fp8_ex(const void* x_fp8, const float* x_scales, const void* gat
  *   NONE v;  RELU max(v, 0), a NaN stays one;  SILU v / (1 + exp(-v));
  *   GELU v (1 + erf(v / sqrt 2)) / 2, within 1e-7 |v|, for v >= -6 also within
  *     1e-5 of itself;
- *   GELU_TANH v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+ *   GELU_TANH v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2
+ * SILU and GELU_TANH are v / (1 + exp(-z)), z = v or 2 sqrt(2 / pi)
+ * (v + 0.044715 v^3): within (5 + 4 max(-z, 0)) 2^-23 of themselves for
+ * z >= -87, and within 2e-36 beyond, where they may be 0.  An infinite v gives
+ * what the formula gives: NaN for -inf. */
 #define LAT_MOE_ACT_NONE 0
 #define LAT_MOE_ACT_RELU 1
 #define LAT_MOE_ACT_SILU 2

@@ -44,7 +44,10 @@ __device__ __forceinline__ float gelu(float v) {
 }
 
 // v / (1 + exp(-z)), with the hardware's reciprocal (1 ulp; a correctly rounded
-// quotient is ten operations, and a gated tile has 64 of them a lane).
+// quotient is ten operations, and a gated tile has 64 of them a lane).  In
+// units of 2^-23: 1 for exp2 and 0.63 z for its argument, which count 1 - s, s
+// the quotient, 1 for the reciprocal, 1/2 each for the sum and the product; z of
+// the tanh is off by up to 2.75 z.  The reciprocal of sums past 2^126, z < -87.3, is 0.
 __device__ __forceinline__ float logistic_times(float v, float z) {
   return v * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
 }

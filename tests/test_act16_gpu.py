@@ -6,8 +6,14 @@ reference makes too.  What is left is the activation's own error, held to the
 bounds that the header states:
 
   gelu       1e-7 |v|, and 1e-5 of itself for v >= -6
+  silu, gelu_tanh, v s(z) with the logistic function s and z = v or
+             2 sqrt(2 / pi) (v + 0.044715 v^3): (5 + 4 max(-z, 0)) 2^-23 of
+             themselves for z >= -87; beyond both are below 2e-36
 
-fp32 outputs below 2^-126 are in steps of 2^-149.
+The last: exp2 and the reciprocal are off by 1 ulp (2^-23), the sum and the
+product by half of one; z log2(e) is off by 0.63 2^-23 z, z of the tanh by up to
+2.75 2^-23 z, which the quotient takes times 1 - s(z), (1 - s(z)) z <= 0.28 for
+z > 0.  fp32 outputs below 2^-126 are in steps of 2^-149.
 """
 import math
 
@@ -22,6 +28,7 @@ if not torch.cuda.is_available():
 import quantized_latent_moe_amd as lm  # noqa: E402
 from tests import _tiles16  # noqa: E402
 
+U = 2.0 ** -23
 STREAMED = [((1, 4099, 72), [-1]), ((4, 8192, 64), [-1]), ((7, 3000, 136), [-1]), ((16, 2050, 264), [-1]),
             ((60, 514, 72), [-1])]
 EXTREME = [0.0, -0.0, 1e-45, -1e-40, 1e-20, -1e-7, 6.0, -6.0, -6.5, 12.0, -12.0, -13.5, 40.0, -40.0, 87.0, -87.0, -88.0,
@@ -31,14 +38,18 @@ EXTREME = [0.0, -0.0, 1e-45, -1e-40, 1e-20, -1e-7, 6.0, -6.0, -6.5, 12.0, -12.0,
 def _reference(v, act):
     """The activation in 64 bits, and what the header allows."""
     v = v.double()
-    assert act == "gelu"
-    ref = v * 0.5 * torch.special.erfc(-v * math.sqrt(0.5))
-    own = torch.where(v >= -6, 1e-5 * ref.abs(), torch.full_like(v, math.inf))
-    return ref, torch.minimum(1e-7 * v.abs(), own)
+    if act == "gelu":
+        ref = v * 0.5 * torch.special.erfc(-v * math.sqrt(0.5))
+        own = torch.where(v >= -6, 1e-5 * ref.abs(), torch.full_like(v, math.inf))
+        return ref, torch.minimum(1e-7 * v.abs(), own)
+    z = v if act == "silu" else 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)
+    ref = v * torch.sigmoid(z)
+    # sigmoid in 64 bits keeps its relative accuracy for z < 0
+    return ref, torch.where(z >= -87, (5 + 4 * (-z).clamp(min=0)) * U * ref.abs(), torch.full_like(v, 2e-36))
 
 
 @pytest.mark.parametrize("case,variants", _tiles16.RAGGED + STREAMED, ids=str)
-@pytest.mark.parametrize("act", ["gelu"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 def test_activation_within_the_stated_bound(case, variants, act):
     T, N, K = case
     assert [v for v, _ in _tiles16.launches(T, N, K)] == variants
