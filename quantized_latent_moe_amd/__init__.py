@@ -502,12 +502,13 @@ def router_topk_ex(logits, k: int, router_idx, router_w, *, bias=None, score: st
     if len(shape) != 2:
         raise ValueError("logits have to be 2-dimensional")
     T, E = shape
+    kept = groups if top_groups is None else top_groups
+    if (E | k | groups | kept) >> 31 not in (0, -1):  # the call would take them modulo 2^32
+        raise ValueError("sizes beyond 32 bits")
     dev = logits.get_device()
     if dev < 0 or dev != cur():
         raise ValueError(f"logits are on {logits.device}: expected the current GPU")
-    if max(E, k, groups, top_groups or 0) >> 31:
-        raise ValueError("sizes beyond 32 bits")
-    rules = Routing(_choice("score", score, SCORES), groups, groups if top_groups is None else top_groups,
+    rules = Routing(_choice("score", score, SCORES), groups, kept,
                     _choice("group_score", group_score, GROUP_SCORES), renormalise, scale)
     rc = (_lib or lib()).lat_moe_router_topk_ex(_tensor("logits", logits, f32, shape, dev),
                                       None if bias is None else _tensor("bias", bias, f32, (E,), dev), T, E, k,
