@@ -284,9 +284,11 @@ typedef struct lat_moe_routing {
  * Weights and their sum are in 64 bits, rounded once.
  * An expert whose logit is -inf or NaN, or whose bias is, is closed: its c is
  * the lowest finite fp32, its weight 0 where it is picked for lack of others
- * (a row without any open expert picks the lowest ids with weights 0), and the
- * second of a group's two largest counts as 0 where it is closed.  A logit of
- * +inf counts as the largest finite fp32, and so does a larger c.
+ * (a row without any open expert picks the lowest ids with weights 0).  The
+ * second of a group's two largest counts as 0 where its c is the lowest finite
+ * fp32: closed, or under a bias of that value.  A logit of +inf counts as the
+ * largest finite fp32, and so does a larger c.  Where the picks' s are all 0
+ * (sigmoids of logits below -104), so are the weights.
  *   logits      [T][E] fp32
  *   bias        [E] fp32, or NULL
  *   routing     host memory, read during the call

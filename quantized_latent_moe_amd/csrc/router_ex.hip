@@ -107,7 +107,8 @@ __device__ __forceinline__ int candidate(float l, float s, float bias) {
 }
 // Below every candidate: an expert that cannot be picked.
 constexpr int kNone = (int)0x80000000u;
-// The fp32 sum of a group's two largest; a closed second counts as 0.
+// The fp32 sum of a group's two largest; a second at the lowest value (closed, or
+// a bias of that value) counts as 0.
 __device__ __forceinline__ int group_score(int m1, int m2, int lowest, bool top2) {
   return top2 && m2 > lowest ? ordered(unordered(m1) + unordered(m2)) : m1;
 }
