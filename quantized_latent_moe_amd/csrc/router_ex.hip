@@ -260,8 +260,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_ex16(const RouterExArgs 
     const uint64_t all = __builtin_amdgcn_ballot_w64(better < a.top_groups);
     const uint32_t kept = (uint32_t)(all >> (lane & 48)) & 0xffffu;
     const float inverse = 1.0f / (float)size;
-    // (e + 1/2) / size is never near a whole number
-    auto is_kept = [&](int e) { return (kept >> ((int)(((float)e + 0.5f) * inverse) * share) & 1u) != 0; };
+    // (e + 1/2) / size is never near a whole number; ids past the last, which stay
+    // out whatever this says, are in groups past the last and shift by any number
+    auto is_kept = [&](int e) { return (kept >> (((int)(((float)e + 0.5f) * inverse) * share) & 31) & 1u) != 0; };
 #pragma unroll
     for (int j = 0; j < Q; ++j) {
       const int e = 64 * j + 4 * l;
