@@ -138,23 +138,6 @@ __device__ __forceinline__ uint2 e4m3_block(const float* v, float& scale) {
                pack_e4m3(v[4] * id, v[5] * id, v[6] * id, v[7] * id)};
 }
 
-// 4 x 4 transpose between four registers and the four 16-lane groups of a
-// wave: register k of group g becomes register g of group k.
-__device__ __forceinline__ void transpose4(uint32_t* r) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const auto v = __builtin_amdgcn_permlane32_swap(r[i], r[i + 2], false, false);
-    r[i] = v[0];
-    r[i + 2] = v[1];
-  }
-#pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    const auto v = __builtin_amdgcn_permlane16_swap(r[i], r[i + 1], false, false);
-    r[i] = v[0];
-    r[i + 1] = v[1];
-  }
-}
-
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
 
 }  // namespace latmoe

@@ -67,6 +67,23 @@ constexpr int kRunBuffers = 4;
 
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 
+// 4 x 4 transpose between four registers and the four 16-lane groups of a
+// wave: register k of group g becomes register g of group k.
+__device__ __forceinline__ void transpose4(uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto v = __builtin_amdgcn_permlane32_swap(r[i], r[i + 2], false, false);
+    r[i] = v[0];
+    r[i + 2] = v[1];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const auto v = __builtin_amdgcn_permlane16_swap(r[i], r[i + 1], false, false);
+    r[i] = v[0];
+    r[i + 1] = v[1];
+  }
+}
+
 // Wait until at most N of this wave's loads and none of its LDS accesses are
 // outstanding, then for the workgroup.  (__syncthreads waits for every load,
 // those of later steps too.)
