@@ -32,6 +32,12 @@ constexpr Dense16Tile kDense16Tiles[] = {
     {64, 32, 1, 0.145f, 0.12f, 3.f},   // 1641 | 114 | 40 | 43
 };
 constexpr int kDense16Variants = 7;
+// Short K, where a tile's beginning and end are most of it and the estimate
+// knows neither: what it picks against the seven tiles in their order (us).
+//   12994 x 64 by 2984  36 | 36 38 36 45 37 48 233    5268 x 64 by 4096  16 | 17 16 18 23 20 26 128
+//   12994 x 264 by 2984 50 | 50 53 51 61 57 73 267    5268 x 264 by 4096 25 | 27 25 27 36 31 42 146
+//   5268 x 264 by 1024  10 | 13 13 10 13 10 13 39     517 x 264 by 4100 9.1 | 23 18 14 9.1 7.9 8.8 20
+// Few tokens with short K could save a microsecond; the rest is the best there is.
 
 // Estimated time of a launch; steps: of K; weight_rows: gated ones counted twice.
 inline float dense16_time(int variant, int64_t T, int64_t weight_rows, int steps, int num_cus) {

@@ -36,8 +36,8 @@
 // to 73% of the cycles; the loop alone, without the loads, runs at 1700 TF.
 // 21000 x 4096 by 4096 with residual takes 565 to 590 us (1190 to 1250 TF; a
 // library product without it 570 to 615 on the same machines), the gated pair
-// 5268 x 4096 by 2 x 8192 495 to 610 us (1160 to 1430 TF), 8192^3 765 us
-// (1430 TF; the library 675 to 750).  Mid-sized ones are bound by what a CU
+// 5268 x 4096 by 2 x 8192 495 to 610 us (1160 to 1430 TF), 8192^3 765 to 790 us
+// (1390 to 1430 TF; the library 675 to 750).  Mid-sized ones are bound by what a CU
 // loads, 75 to 100 GB/s with all of them at it: 5268 x 4096 by 1024 takes 50 us
 // (870 TF), 517 x 2056 by 4100 25 us, 5268 x 4096 by 128 15 us.
 #include "dense16_tiles.h"

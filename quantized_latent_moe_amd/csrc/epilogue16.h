@@ -232,6 +232,10 @@ struct TileEpilogue {
   // q8_1 alone) and a residual of type RT (or none): types and places are known
   // here, and pointers go from row to row.  The general form below takes 50 VALU
   // operations for each 8 columns, 4 us for a tile of 256 x 256; this one 15.
+  // Calls that have to take the general one (us, by 4096 x 4096 with 21000
+  // tokens): fp32 y with a 16-bit residual 624 (fp32 residual, here: 615), y or
+  // residual of the other 16-bit type 551 to 595 (of the same: 543 to 564),
+  // q8_1 with a residual 596 to 602 or beside an fp32 y 612 (alone: 545).
   static constexpr int kNone = -1;
   template <int YT, int RT>
   static __device__ __forceinline__ void run_whole(const Epilogue16& e, const v4f (&acc)[FA][FB], float* lds, int n0,

@@ -10,10 +10,10 @@
 //
 // Up to 256 experts, 16 picks and 16 groups, 16 lanes take a token, so that a
 // wave's VALU works on four and a maximum is four DPP steps.  What bounds it:
-// many tokens the VALU (21000 x 256 in 8 groups, 8 picks: 1400 operations for
-// four tokens, of them 36 for a score of each lane and 43 for a round of
-// picking; 19.3 us, without groups 15.7, 5268 x 128 without groups 5.6), few
-// tokens the rounds, one behind the other (4 x 128 5.1 us, without groups 4.1).
+// many tokens the VALU (21000 x 256 in 8 groups, 8 picks: 1420 operations for
+// four tokens, of them 37 for a score of each lane and 43 for a round of
+// picking; 19.8 us, without groups 16, 5268 x 128 without groups 5.6), few
+// tokens the rounds, one behind the other (4 x 128 5.1 us, without groups 4.2).
 // A wave for each token takes 36 to 44 us for 21000 x 256, and 5.8 for 4 x 128.
 #include "block_fp8.h"
 #include "exp64.h"
@@ -315,7 +315,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_ex16(const RouterExArgs 
 }
 
 // Any other call: a wave takes a token, lane l experts l, l + 64, ...; a lane
-// for each group.  P: experts a lane (E <= 64 P).
+// for each group.  P: experts a lane (E <= 64 P).  In 8 groups, 8 picks:
+// 512 experts take 9.6 us for 4 tokens, 21 for 5268 and 57 for 21000, 1024
+// experts 15, 33 and 100 (their bytes: 17), bound by the rounds' reductions
+// over 64 lanes.
 template <int P>
 __global__ __launch_bounds__(64 * kWaves) void k_router_ex(const RouterExArgs a) {
   __shared__ int lds[kWaves][64 * P];
